@@ -68,6 +68,17 @@ enum { KQ_OP_ACCUMULATE_COV = 0, KQ_OP_BIIP = 1, KQ_OP_CHOLESKY = 2, KQ_OP_OBS =
 #define KQ_DECODE_MAX_LAYERS 4  /* layers per kq_decode_matvec_group call */
 #define KQ_DECODE_NOALLOC_SCRATCH 2228224  /* bytes of the fixed scratch of kq_decode_matvec_group_noalloc */
 
+/* kq_cache_append flags. */
+enum { KQ_ROPE_INTERLEAVED = 1 /* rotate the pairs (2j, 2j+1) instead of (j, j + rot_dim / 2) */ };
+
+/* Bits of the info word of the kq_cache_* calls (set by device-side checks, never cleared). */
+enum {
+  KQ_INFO_ROWS = 1,     /* q_start not ascending, outside [0, rows], or a sequence with more than max_q new tokens */
+  KQ_INFO_LENGTH = 2,   /* a length below 0, above max_pages * page, or (append, read) below the new tokens */
+  KQ_INFO_PAGE = 4,     /* a page number outside [0, pages) */
+  KQ_INFO_POSITION = 8  /* a position at or past rope_len */
+};
+
 /*
  * Rotation of one side: U = (Q_m kron H_p / sqrt(p)) diag(sigma), n = m * p,
  * p = 2^log2p, m odd. H_p is the Sylvester Hadamard matrix,
@@ -446,6 +457,145 @@ kq_status kq_decode_matvec_group_noalloc(const kq_decode_layer* layers, int32_t 
                                          int32_t bits, int32_t group, const double* s_x,
                                          const kq_rot* rot_in, const float* x, int64_t tokens,
                                          void* stream);
+
+/*
+ * The 8-bit key/value cache: what a decoder block needs between its q/k/v and
+ * its o projection when the weights are served by kq_decode_matvec_group.
+ *
+ * Keys and values are held as signed 8-bit codes in pages of `page` tokens,
+ * with one float32 scale for each page and key/value head (a block): a value
+ * is code * scale. A block's scale only grows while its page fills, so it
+ * covers the largest entry that the block has held.
+ *   k        device int8 [pages, kv_heads, page, head_dim]
+ *   v        device int8 [pages, kv_heads, page / 16, head_dim, 16]: the 16
+ *            tokens of a group lie side by side for each channel, which is the
+ *            order the attention's product with the values reads them in
+ *   k_scale, v_scale  device float32 [pages, kv_heads], as kq_cache_append
+ *            writes them: 0 for a block of zeros (its codes are 0), else from
+ *            2^-100 up; NaN for a block that was given a NaN or an infinity
+ *   page     16, 32, 64 or 128
+ *   head_dim 64 or 128
+ * k and v are 16-byte aligned.
+ */
+typedef struct {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages;
+  int32_t page;
+  int32_t kv_heads;
+  int32_t head_dim;
+} kq_cache;
+
+/*
+ * The sequences of one call. Sequence b holds seq_lens[b] tokens, this call's
+ * new ones included; the call's rows q_start[b] .. q_start[b+1]-1 are its last
+ * ones. Token position p is in page table[b][p / page], slot p mod page. The
+ * arrays are read on the device, so a captured graph replays with what they
+ * hold at replay time, within the bounds given here.
+ *   table     device int32 [batch, max_pages]; entries past a sequence's last page are not read
+ *   seq_lens  device int32 [batch], each in [0, max_pages * page]
+ *   q_start   device int32 [batch + 1], ascending, within [0, rows]; rows at or
+ *             past q_start[batch] are neither read nor written
+ *   max_q     no sequence has more than max_q rows
+ *   max_pages * page < 2^31
+ * What the host cannot see is checked on the device: a wrong entry sets a bit
+ * of the call's info word (KQ_INFO_*) and is never followed out of bounds.
+ */
+typedef struct {
+  const int32_t* table;
+  const int32_t* seq_lens;
+  const int32_t* q_start;
+  int32_t batch;
+  int32_t max_pages;
+  int32_t max_q;
+} kq_cache_batch;
+
+/*
+ * kq_cache_append -- rotate new queries and keys, quantize new keys and values
+ * into the cache
+ *
+ * For every new token at position p = seq_lens[b] - n_b + i (n_b rows, i the
+ * row's place among them) and every head of q and k:
+ *   y_j = w_j x_j / sqrt(mean_j x_j^2 + eps)      (with q_norm / k_norm; else y = x)
+ *   (a, c) -> (a cos - c sin, c cos + a sin)      (with rope) over the pairs
+ *             (j, j + rot_dim/2) or, KQ_ROPE_INTERLEAVED, (2j, 2j+1), j < rot_dim/2;
+ *             entries from rot_dim on pass unrotated
+ * q is rounded once to its type and written to q_out. A block (page, head)
+ * that takes new keys, A their largest magnitude, gets the scale
+ *   s = max(s_old, A > 0 ? max(float32(A / 127), 2^-100) : 0)
+ * (s_old 0 where the page's first slot is among the new tokens) and the codes
+ * round_half_even(y / s) in [-127, 127]; codes already in the block become
+ * round_half_even(code s_old / s) where s grew. Values likewise, unrotated.
+ * A NaN or infinity makes the block's scale NaN: all of it reads as NaN.
+ *   q        device [rows, heads, head_dim] of type dtype, row pitch ldq elements,
+ *            or NULL (then heads 0, no q_out); q_out likewise, pitch ldqo; may equal q
+ *   k, v     device [rows, kv_heads, head_dim], row pitches ldk, ldv
+ *   dtype    KQ_BF16 or KQ_F32; pointers 16-byte aligned, pitches multiples of 16 bytes
+ *   q_norm, k_norm  device float32 [head_dim] or NULL (no norm on that side); eps > 0
+ *   rope     device float32 [rope_len, rot_dim], row p: rot_dim/2 cosines, then
+ *            rot_dim/2 sines, or NULL (no rotation); rot_dim a multiple of 4, <= head_dim
+ *   info     device int32 or NULL: KQ_INFO_* bits are or-ed in; the caller sets it to 0 first
+ * A token whose position is negative (fewer tokens in the cache than rows) or
+ * past the table of rotations reads as NaN in q_out; the former is not stored.
+ * A token of a bad page is not stored. Pages that the call writes belong to
+ * one sequence each. Norm, rotation and rounding run in float64, so that codes
+ * do not depend on the order of operations.
+ */
+kq_status kq_cache_append(const kq_cache* cache, const kq_cache_batch* batch, const void* q, const void* k,
+                          const void* v, int32_t dtype, int64_t rows, int32_t heads, int64_t ldq, int64_t ldk,
+                          int64_t ldv, const float* q_norm, const float* k_norm, float eps, const float* rope,
+                          int64_t rope_len, int32_t rot_dim, uint32_t flags, void* q_out, int64_t ldqo,
+                          int32_t* info, void* stream);
+
+/*
+ * kq_cache_read -- cached keys and values back as floating values
+ *
+ * Row q_start[b] + i of k_out and v_out becomes code * scale (float32, rounded
+ * once to dtype) of position seq_lens[b] - n_b + i, for checks, hand-over or a
+ * longer store elsewhere.
+ *   k_out, v_out  device [rows, kv_heads, head_dim] of type dtype (KQ_BF16 or KQ_F32), row
+ *            pitches ldk, ldv; 16-byte aligned, pitches multiples of 16 bytes; either may be NULL
+ *   info     as kq_cache_append
+ * Rows of a bad page or a negative position read as NaN.
+ */
+kq_status kq_cache_read(const kq_cache* cache, const kq_cache_batch* batch, void* k_out, void* v_out, int32_t dtype,
+                        int64_t rows, int64_t ldk, int64_t ldv, int32_t* info, void* stream);
+
+/*
+ * kq_cache_attention -- attention of the new tokens' queries over the cache
+ *
+ * Row i of sequence b, at position p = seq_lens[b] - n_b + i, head h (key/value
+ * head h / (heads / kv_heads)):
+ *   out = sum_t softmax_t(scale q . k_t) v_t over t in [0, p], or, window > 0,
+ *   t in (p - window, p]
+ * A row that sees no token (p < 0) becomes 0. A few rows a sequence (single
+ * tokens, drafts) and prompts run different kernels; the context is split over
+ * workgroups and joined by a second launch where the rows alone do not fill
+ * the GPU. Products run on float16 MFMA with float32 sums: codes are exact
+ * there, a bf16 query is (scaled by a power of two), a float32 query and, for
+ * float32 outputs, the softmax weights are two float16 pieces (22 bits).
+ *   q        device [rows, heads, head_dim] of type dtype (KQ_BF16 or KQ_F32), row pitch ldq
+ *   out      device, same shape and type, row pitch ldo; must not overlap q
+ *            (16-byte aligned, pitches multiples of 16 bytes)
+ *   heads    a multiple of kv_heads
+ *   scale    finite and > 0; window >= 0
+ *   info     as kq_cache_append (rows past max_q of a sequence are left as they were)
+ *   ws       kq_cache_attention_workspace bytes; calls sharing it must not overlap.
+ * Tokens of a bad page count as NaN. Sums have a fixed order (deterministic).
+ */
+kq_status kq_cache_attention(const kq_cache* cache, const kq_cache_batch* batch, const void* q, int32_t dtype,
+                             int64_t rows, int32_t heads, int64_t ldq, float scale, int32_t window, void* out,
+                             int64_t ldo, int32_t* info, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Bytes of scratch space of kq_cache_attention for these bounds (host; reads
+ * the sizes of the two structs, not their pointers). What it returns for
+ * window 0 is enough for every window. (size_t)-1 for sizes that the call refuses.
+ */
+size_t kq_cache_attention_workspace(const kq_cache* cache, const kq_cache_batch* batch, int32_t dtype, int64_t rows,
+                                    int32_t heads, int32_t window);
 
 #ifdef __cplusplus
 }

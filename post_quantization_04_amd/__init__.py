@@ -24,6 +24,8 @@ __all__ = [
     "decode_matvec_group_noalloc", "decode_workspace", "kron_loss", "Rot", "KQ_DECODE_NOALLOC_SCRATCH",
     "DecodeLayer", "accumulate_xcov", "biip_transform", "gptaq_target",
     "timing_enable", "timing_query",
+    "KVCache", "CacheBatch", "cache_append", "cache_read", "cache_attention", "cache_attention_workspace",
+    "KQ_ROPE_INTERLEAVED", "KQ_INFO_ROWS", "KQ_INFO_LENGTH", "KQ_INFO_PAGE", "KQ_INFO_POSITION",
 ]
 
 KQ_OK, KQ_EINVAL, KQ_ENOTPD, KQ_EINFEASIBLE, KQ_EDEVICE, KQ_EUNSUPPORTED = range(6)
@@ -35,6 +37,8 @@ KQ_OP_XCOV, KQ_OP_GPTAQ = 6, 7
 KQ_DECODE_MAX_TOKENS = 4
 KQ_DECODE_MAX_LAYERS = 4
 KQ_DECODE_NOALLOC_SCRATCH = 2228224
+KQ_ROPE_INTERLEAVED = 1
+KQ_INFO_ROWS, KQ_INFO_LENGTH, KQ_INFO_PAGE, KQ_INFO_POSITION = 1, 2, 4, 8
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -62,6 +66,21 @@ class DecodeLayer(ctypes.Structure):
     _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
                 ("dout", ctypes.c_int64), ("s_g", ctypes.c_void_p), ("rot_out", ctypes.POINTER(Rot)),
                 ("y", ctypes.c_void_p)]
+
+
+class CacheStruct(ctypes.Structure):
+    """kq_cache: the code and scale arrays of an 8-bit key/value cache."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class CacheBatchStruct(ctypes.Structure):
+    """kq_cache_batch: the sequences of one call over a cache."""
+
+    _fields_ = [("table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_q", ctypes.c_int32)]
 
 
 _LIB = None
@@ -107,10 +126,18 @@ def lib() -> ctypes.CDLL:
                                          ctypes.POINTER(Rot), _VP, _I64, _VP, _SZ, _VP]
     L.kq_decode_matvec_group_noalloc.argtypes = [ctypes.POINTER(DecodeLayer), _I32, _I64, _I32, _I32, _VP,
                                                  ctypes.POINTER(Rot), _VP, _I64, _VP]
+    cache, batch = ctypes.POINTER(CacheStruct), ctypes.POINTER(CacheBatchStruct)
+    L.kq_cache_append.argtypes = [cache, batch, _VP, _VP, _VP, _I32, _I64, _I32, _I64, _I64, _I64, _VP, _VP, _F32, _VP,
+                                  _I64, _I32, _U32, _VP, _I64, _VP, _VP]
+    L.kq_cache_read.argtypes = [cache, batch, _VP, _VP, _I32, _I64, _I64, _I64, _VP, _VP]
+    L.kq_cache_attention.argtypes = [cache, batch, _VP, _I32, _I64, _I32, _I64, _F32, _I32, _VP, _I64, _VP, _VP, _SZ, _VP]
+    L.kq_cache_attention_workspace.argtypes = [cache, batch, _I32, _I64, _I32, _I32]
+    L.kq_cache_attention_workspace.restype = _SZ
     for name in ("kq_accumulate_cov", "kq_sensitivity", "kq_allocate_bits", "kq_biip_rotate",
                  "kq_cholesky_inv", "kq_obs_quantize", "kq_pack_codes", "kq_decode_matvec",
                  "kq_decode_matvec_group", "kq_decode_matvec_group_noalloc", "kq_kron_loss",
-                 "kq_accumulate_xcov", "kq_biip_transform", "kq_gptaq_target"):
+                 "kq_accumulate_xcov", "kq_biip_transform", "kq_gptaq_target", "kq_cache_append", "kq_cache_read",
+                 "kq_cache_attention"):
         getattr(L, name).restype = ctypes.c_int
     _LIB = L
     return L
@@ -431,3 +458,193 @@ def decode_matvec_group_noalloc(layers, bits: int, group: int, s_x, rot_in: Opti
     _check(lib().kq_decode_matvec_group_noalloc(arr, len(layers), din, bits, group, _ptr(s_x),
                                                 None if rot_in is None else ctypes.byref(rot_in), _ptr(x), tokens,
                                                 _stream(stream)), "kq_decode_matvec_group_noalloc")
+
+
+class KVCache:
+    """An 8-bit paged key/value cache (kq_cache): int8 codes k [pages, kv_heads, page, head_dim] and
+    v [pages, kv_heads, page / 16, head_dim, 16] (16 tokens of a channel side by side) with float32 scales
+    k_scale, v_scale [pages, kv_heads]. Holds the tensors; the calls write into them."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "device", "kv_heads", "head_dim", "page", "struct", "ref")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        _need(k.dim() == 4 and v.dim() == 5, "KVCache: k is [pages, kv_heads, page, head_dim], "
+                                             "v is [pages, kv_heads, page / 16, head_dim, 16]")
+        pages, heads, page, dim = k.shape
+        _need(tuple(v.shape) == (pages, heads, page // 16, dim, 16) and page % 16 == 0, "KVCache: k and v differ in shape")
+        _need(tuple(k_scale.shape) == tuple(v_scale.shape) == (pages, heads), "KVCache: scales are [pages, kv_heads]")
+        _need(k.dtype == v.dtype == torch.int8 and k_scale.dtype == v_scale.dtype == torch.float32, "KVCache: dtypes")
+        _need(all(t.is_contiguous() and t.device == k.device for t in (k, v, k_scale, v_scale)),
+              "KVCache: tensors must be contiguous and on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device, self.kv_heads, self.head_dim, self.page = k.device, heads, dim, page
+        self.struct = CacheStruct(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), pages, page, heads, dim)
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def allocate(cls, pages: int, page: int, kv_heads: int, head_dim: int, device) -> "KVCache":
+        """A cache of zeros."""
+        import torch
+        _need(page in (16, 32, 64, 128), "KVCache: page must be 16, 32, 64 or 128")
+        scale = torch.zeros((2, pages, kv_heads), dtype=torch.float32, device=device)
+        return cls(torch.zeros((pages, kv_heads, page, head_dim), dtype=torch.int8, device=device),
+                   torch.zeros((pages, kv_heads, page // 16, head_dim, 16), dtype=torch.int8, device=device),
+                   scale[0], scale[1])
+
+
+class CacheBatch:
+    """The sequences of one call over a cache (kq_cache_batch): table int32 [batch, max_pages], seq_lens int32
+    [batch] (tokens in the cache, this call's included), q_start int32 [batch + 1] (row ranges), max_q a bound
+    on a sequence's rows. The calls read the tensors on the device each time, so a serving loop updates them
+    in place and keeps the object."""
+
+    __slots__ = ("table", "seq_lens", "q_start", "max_q", "device", "struct", "ref")
+
+    def __init__(self, table, seq_lens, q_start, max_q: int):
+        import torch
+        _need(table.dim() == 2 and seq_lens.dim() == 1 and q_start.dim() == 1 and table.shape[0] == seq_lens.shape[0]
+              and q_start.shape[0] == table.shape[0] + 1, "CacheBatch: table [batch, max_pages], seq_lens [batch], "
+                                                          "q_start [batch + 1]")
+        _need(table.dtype == seq_lens.dtype == q_start.dtype == torch.int32, "CacheBatch: int32 tensors")
+        _need(all(t.is_contiguous() and t.device == table.device for t in (table, seq_lens, q_start)),
+              "CacheBatch: tensors must be contiguous and on one device")
+        _need(0 <= max_q < 2 ** 31, "CacheBatch: max_q out of range")
+        self.table, self.seq_lens, self.q_start, self.max_q = table, seq_lens, q_start, int(max_q)
+        self.device = table.device
+        self.struct = CacheBatchStruct(_ptr(table), _ptr(seq_lens), _ptr(q_start), table.shape[0], table.shape[1],
+                                       self.max_q)
+        self.ref = ctypes.byref(self.struct)
+
+
+_CACHE_DTYPES = None
+
+
+def _cache_tensor(name: str, t, heads: int, cache: KVCache, rows: Optional[int] = None, dtype=None):
+    """(rows, row pitch) of a [rows, heads, head_dim] tensor of a cache call."""
+    shape = t.shape
+    _need(len(shape) == 3 and shape[2] == cache.head_dim and (heads == 0 or shape[1] == heads)
+          and (rows is None or shape[0] == rows), f"{name}: must be [rows, heads, head_dim]")
+    _need(dtype is None or t.dtype == dtype, f"{name}: dtype differs")
+    _need(t.device == cache.device, f"{name}: on another device than the cache")
+    stride = t.stride()
+    n, wide = shape[0], shape[1] * shape[2]
+    _need(stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1 or n == 0),
+          f"{name}: a row's heads must be contiguous")
+    return n, (stride[0] if n > 1 else wide)
+
+
+def _cache_dtype(name: str, t) -> int:
+    global _CACHE_DTYPES
+    if _CACHE_DTYPES is None:
+        import torch
+        _CACHE_DTYPES = {torch.bfloat16: KQ_BF16, torch.float32: KQ_F32}
+    d = _CACHE_DTYPES.get(t.dtype)
+    _need(d is not None, f"{name}: bfloat16 or float32")
+    return d
+
+
+def _cache_info(name: str, info, cache: KVCache):
+    if info is not None:
+        import torch
+        _need(info.dtype == torch.int32 and info.numel() >= 1 and info.device == cache.device,
+              f"{name}: info must be an int32 tensor on the cache's device")
+    return _ptr(info)
+
+
+def _cache_call(name: str, fn, cache: KVCache, batch: CacheBatch, args, stream) -> None:
+    """fn(cache, batch, *args, stream) on the cache's device, whichever device is current."""
+    import torch
+    device = cache.device
+    _need(device.type == "cuda" and batch.device == device, f"{name}: cache and batch must be on one GPU")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    else:
+        _need(stream.device == device, f"{name}: the stream belongs to another device")
+    if torch.cuda.current_device() == device.index:
+        status = fn(cache.ref, batch.ref, *args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(cache.ref, batch.ref, *args, stream.cuda_stream)
+    if status != KQ_OK:
+        _check(status, name)
+
+
+def cache_append(cache: KVCache, batch: CacheBatch, q, k, v, q_out=None, *, q_norm=None, k_norm=None,
+                 eps: float = 1e-6, rope=None, interleaved: bool = False, info=None, stream=None) -> None:
+    """Norm and rotate new queries and keys, quantize new keys and values into the cache. q [rows, heads, head_dim]
+    (or None), k and v [rows, kv_heads, head_dim], bfloat16 or float32, row pitches free; q_out like q (may be q).
+    q_norm, k_norm: float32 [head_dim]; rope: float32 [positions, rot_dim], cosines then sines (pipeline.rope_table);
+    info: int32 device tensor for KQ_INFO_* bits, zeroed by the caller."""
+    import torch
+    name = "cache_append"
+    dtype = _cache_dtype(name, k)
+    rows, ldk = _cache_tensor("cache_append: k", k, cache.kv_heads, cache)
+    _, ldv = _cache_tensor("cache_append: v", v, cache.kv_heads, cache, rows, k.dtype)
+    heads = ldq = ldqo = 0
+    _need((q is None) == (q_out is None), "cache_append: q and q_out come together")
+    if q is not None:
+        heads = q.shape[1]
+        _, ldq = _cache_tensor("cache_append: q", q, heads, cache, rows, k.dtype)
+        _, ldqo = _cache_tensor("cache_append: q_out", q_out, heads, cache, rows, k.dtype)
+    for w in (q_norm, k_norm):
+        if w is not None:
+            _need(w.dtype == torch.float32 and w.shape == (cache.head_dim,) and w.stride(0) == 1
+                  and w.device == cache.device, "cache_append: norm weights are float32 [head_dim] on the cache's device")
+    rope_len = rot = 0
+    if rope is not None:
+        _need(rope.dim() == 2 and rope.dtype == torch.float32 and rope.is_contiguous() and rope.device == cache.device,
+              "cache_append: rope is contiguous float32 [positions, rot_dim] on the cache's device")
+        rope_len, rot = rope.shape
+    _cache_call(name, lib().kq_cache_append, cache, batch,
+                (_ptr(q), k.data_ptr(), v.data_ptr(), dtype, rows, heads, ldq, ldk, ldv, _ptr(q_norm), _ptr(k_norm), eps,
+                 _ptr(rope), rope_len, rot, KQ_ROPE_INTERLEAVED if interleaved else 0, _ptr(q_out), ldqo,
+                 _cache_info(name, info, cache)), stream)
+
+
+def cache_read(cache: KVCache, batch: CacheBatch, k_out, v_out, *, info=None, stream=None) -> None:
+    """The last n_b = q_start[b + 1] - q_start[b] cached tokens of every sequence as values: k_out, v_out
+    [rows, kv_heads, head_dim], bfloat16 or float32 (one may be None)."""
+    name = "cache_read"
+    one = k_out if k_out is not None else v_out
+    _need(one is not None, "cache_read: neither k_out nor v_out")
+    dtype = _cache_dtype(name, one)
+    rows, ldk = _cache_tensor("cache_read: output", one, cache.kv_heads, cache)
+    ldv = ldk
+    if k_out is not None and v_out is not None:
+        _, ldv = _cache_tensor("cache_read: v_out", v_out, cache.kv_heads, cache, rows, k_out.dtype)
+    _cache_call(name, lib().kq_cache_read, cache, batch,
+                (_ptr(k_out), _ptr(v_out), dtype, rows, ldk, ldv, _cache_info(name, info, cache)), stream)
+
+
+def cache_attention_workspace(cache: KVCache, batch: CacheBatch, q, window: int = 0):
+    """A workspace for cache_attention with queries like q (window 0: enough for every window). Calls that share
+    it must not overlap."""
+    import torch
+    need = lib().kq_cache_attention_workspace(cache.ref, batch.ref, _cache_dtype("cache_attention", q), q.shape[0],
+                                              q.shape[1], window)
+    if need == ctypes.c_size_t(-1).value:
+        raise KQError(KQ_EINVAL, "kq_cache_attention_workspace: invalid sizes")
+    return torch.empty(need, dtype=torch.uint8, device=cache.device)
+
+
+def cache_attention(cache: KVCache, batch: CacheBatch, q, out, *, scale: Optional[float] = None, window: int = 0,
+                    info=None, ws=None, stream=None) -> None:
+    """out <- attention of q [rows, heads, head_dim] over the cached tokens up to each row's own position (the last
+    ``window`` of them with window > 0); out like q. scale defaults to head_dim^-1/2."""
+    import torch
+    name = "cache_attention"
+    dtype = _cache_dtype(name, q)
+    heads = q.shape[1] if q.dim() == 3 else 0
+    rows, ldq = _cache_tensor("cache_attention: q", q, heads, cache)
+    _, ldo = _cache_tensor("cache_attention: out", out, heads, cache, rows, q.dtype)
+    if ws is None:
+        ws = cache_attention_workspace(cache, batch, q, window)
+        if stream is not None:
+            ws.record_stream(stream)
+    else:
+        _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == cache.device,
+              "cache_attention: ws is contiguous uint8 on the cache's device")
+    _cache_call(name, lib().kq_cache_attention, cache, batch,
+                (q.data_ptr(), dtype, rows, heads, ldq, cache.head_dim ** -0.5 if scale is None else scale, window,
+                 out.data_ptr(), ldo, _cache_info(name, info, cache), ws.data_ptr(), ws.numel(), ), stream)

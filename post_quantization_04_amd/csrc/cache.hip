@@ -1,0 +1,516 @@
+// The 8-bit key/value cache: appending to it (norm, rotation, quantization in one launch) and
+// reading it back.
+//
+// Append. A block (page, head) of new tokens is quantized on one scale, so its largest entry has
+// to be known before its first code: one workgroup holds a whole block of one side (keys or
+// values) in registers, a wave for each 16 slots, two adjacent channels a lane (64 lanes a row at
+// head_dim 128, two rows of 32 lanes at 64). Each value is read once and each code written once;
+// the layout of the values (16 tokens of a channel side by side) makes a lane's 16 slots one
+// 16-byte store for each of its channels. Queries need no scale and go to workgroups of their
+// own in the same launch, a wave for each token and group of heads.
+//
+// Arithmetic is float64 from the loaded value to the code: with float32 a norm, a rotation and
+// a division end within 1e-5 of a step of a rounding border for one entry in 10^5, whose code
+// then depends on the order of operations. A float64 operation issues at float32's rate on
+// gfx950.
+#include <cmath>
+
+#include "cache_internal.h"
+
+namespace kq {
+namespace {
+
+constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100: keeps 1 / scale and its sums finite
+
+struct AppendArgs {
+  SeqArgs seq;
+  const void* src[3];     // q, k, v
+  int64_t ld[3];
+  const float* norm[2];   // q, k
+  double eps;
+  const float* rope;
+  int64_t rope_len;
+  int rot;
+  int interleaved;
+  void* q_out;
+  int64_t ldqo;
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int heads, kvh;
+  int blocks;             // blocks a sequence's new tokens can touch
+  int batch;
+  int64_t kv_wgs;         // workgroups before the queries'
+  int q_groups;           // head groups of a token in the query part
+};
+
+template <bool BF16>
+__device__ __forceinline__ float2 load2(const void* p, int64_t at) {
+  if (BF16) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(p) + at);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  return *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(p) + at);
+}
+
+// Sum over the LPR lanes of a row, the same value in all of them.
+template <int LPR>
+__device__ __forceinline__ double row_sum(double v) {
+#pragma unroll
+  for (int o = 1; o < LPR; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Norm and rotation of a row's entries e = 2 l and 2 l + 1 in the lanes of that row. w: the
+// norm's weights of the two (with `norm`), cs: this position's row of the table.
+template <int D>
+__device__ __forceinline__ void place(double& y0, double& y1, bool norm, float2 w, double eps, const float* cs, int rot,
+                                      bool interleaved, int l) {
+  constexpr int LPR = D / 2;
+  if (norm) {
+    const double r = 1.0 / sqrt(row_sum<LPR>(y0 * y0 + y1 * y1) * (1.0 / D) + eps);
+    y0 *= r * double(w.x);
+    y1 *= r * double(w.y);
+  }
+  if (cs) {
+    const int half = rot >> 1;
+    if (interleaved) {
+      if (2 * l < rot) {
+        const double c = cs[l], s = cs[half + l];
+        const double a = y0;
+        y0 = a * c - y1 * s;
+        y1 = y1 * c + a * s;
+      }
+    } else {
+      // entry e < half pairs with e + half, held rot / 4 lanes on (every lane takes part in the exchange)
+      const int lane = threadIdx.x & 63;
+      const bool low = 2 * l < half, in = 2 * l < rot;
+      const int from = in ? (low ? lane + (rot >> 2) : lane - (rot >> 2)) : lane;
+      const double p0 = __shfl(y0, from), p1 = __shfl(y1, from);
+      if (in) {
+        const int j = low ? 2 * l : 2 * l - half;
+        const double c0 = cs[j], c1 = cs[j + 1];
+        const double s0 = low ? -double(cs[half + j]) : double(cs[half + j]);
+        const double s1 = low ? -double(cs[half + j + 1]) : double(cs[half + j + 1]);
+        y0 = y0 * c0 + p0 * s0;
+        y1 = y1 * c1 + p1 * s1;
+      }
+    }
+  }
+}
+
+// round_half_even(y / s) in [-127, 127], inv = 1 / s: the product is within 1e-13 of the quotient,
+// so only a value that close to a border needs the division itself.
+__device__ __forceinline__ int code_of(double y, double s, double inv) {
+  const double t = y * inv;
+  double r = rint(t);
+  if (fabs(fabs(t - r) - 0.5) < 1e-12) r = rint(y / s);
+  return int(fmin(fmax(r, -127.0), 127.0));
+}
+
+__device__ __forceinline__ int rescaled(int code, double ratio) { return int(rint(double(code) * ratio)); }
+
+// One block of one side. NS 1: the block takes one new token (slot lo), which every lane computes.
+template <bool BF16, int D, int PAGE, int NS>
+__device__ void append_block(const AppendArgs& a, bool is_v, int head, int pageid, int pos0, int lo, int hi, int row_lo) {
+  constexpr int LPR = D / 2, SL = 16 * LPR / 64;  // lanes a row, slots a lane
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int l = lane & (LPR - 1), hh = lane / LPR;
+  const int first_slot = 16 * w + hh * SL;
+  const bool norm = !is_v && a.norm[1] != nullptr;
+  const bool turn = !is_v && a.rope != nullptr;
+  const void* src = is_v ? a.src[2] : a.src[1];
+  const int64_t ld = is_v ? a.ld[2] : a.ld[1];
+  const float2 wt = norm ? *reinterpret_cast<const float2*>(a.norm[1] + 2 * l) : make_float2(1.0f, 1.0f);
+  float* const scale_at = (is_v ? a.v_scale : a.k_scale) + int64_t(pageid) * a.kvh + head;
+  const float s_old = lo > 0 ? *scale_at : 0.0f;
+
+  double y[NS][2];
+  const bool mine = NS == 1 || (16 * w < hi && 16 * w + 16 > lo);  // uniform in the wave
+  double amax = 0.0;
+  if (mine) {
+    float2 x[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int slot = NS == 1 ? lo : min(max(first_slot + s, lo), hi - 1);
+      x[s] = load2<BF16>(src, int64_t(row_lo + slot - lo) * ld + int64_t(head) * D + 2 * l);
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int slot = NS == 1 ? lo : first_slot + s;
+      const int64_t p = pos0 + min(max(slot, lo), hi - 1);
+      y[s][0] = x[s].x;
+      y[s][1] = x[s].y;
+      const bool off = turn && p >= a.rope_len;
+      place<D>(y[s][0], y[s][1], norm, wt, a.eps, turn ? a.rope + (off ? 0 : p) * a.rot : nullptr, a.rot,
+               a.interleaved, l);
+      if (slot >= lo && slot < hi) {
+        if (off) {
+          report(a.seq.info, KQ_INFO_POSITION);
+          y[s][0] = NAN;
+        }
+        // infinite for a NaN too, which a plain maximum would drop
+        amax = fmax(amax, fabs(y[s][0]) < INFINITY ? fabs(y[s][0]) : INFINITY);
+        amax = fmax(amax, fabs(y[s][1]) < INFINITY ? fabs(y[s][1]) : INFINITY);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) amax = fmax(amax, __shfl_xor(amax, o));
+  if (PAGE > 16) {
+    __shared__ double top[PAGE / 16];
+    if (lane == 0) top[w] = amax;
+    __syncthreads();  // also: every wave has read the old scale before it is replaced
+#pragma unroll
+    for (int i = 0; i < PAGE / 16; ++i) amax = fmax(amax, top[i]);
+  }
+  float s_new = amax > 0.0 ? fmaxf(float(amax / 127.0), kScaleFloor) : 0.0f;
+  if (!(s_new >= s_old)) s_new = s_old;                       // a NaN of the block stays
+  if (!(amax < INFINITY) || !(s_new < INFINITY)) s_new = NAN;
+  if (threadIdx.x == 0) *scale_at = s_new;
+  const double sd = s_new, inv = s_new > 0.0f ? 1.0 / sd : 0.0;
+  const bool usable = s_new > 0.0f;                           // not 0, not NaN
+  const bool grow = lo > 0 && s_old > 0.0f && s_new > s_old;
+  const double ratio = grow ? double(s_old) / sd : 1.0;
+  const bool old_here = grow && 16 * w < lo;
+  const bool new_here = 16 * w < hi && 16 * w + 16 > lo;
+  if (!old_here && !new_here) return;
+
+  int c[NS][2];
+  if (mine) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) c[s][e] = usable ? code_of(y[s][e], sd, inv) : 0;
+  }
+  const int64_t block = int64_t(pageid) * a.kvh + head;
+  if (!is_v) {
+    int8_t* const rows = a.k + block * (PAGE * D) + 2 * l;
+    if (NS == 1) {
+      if (new_here && hh == 0) *reinterpret_cast<uint16_t*>(rows + lo * D) = uint16_t((c[0][0] & 255) | ((c[0][1] & 255) << 8));
+    } else if (new_here) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int slot = first_slot + s;
+        if (slot >= lo && slot < hi)
+          *reinterpret_cast<uint16_t*>(rows + slot * D) = uint16_t((c[s][0] & 255) | ((c[s][1] & 255) << 8));
+      }
+    }
+    if (old_here) {
+      uint16_t o[SL];
+#pragma unroll
+      for (int s = 0; s < SL; ++s) o[s] = *reinterpret_cast<const uint16_t*>(rows + (first_slot + s) * D);
+#pragma unroll
+      for (int s = 0; s < SL; ++s)
+        if (first_slot + s < lo)
+          *reinterpret_cast<uint16_t*>(rows + (first_slot + s) * D) =
+              uint16_t((rescaled(int8_t(o[s] & 255), ratio) & 255) | ((rescaled(int8_t(o[s] >> 8), ratio) & 255) << 8));
+    }
+    return;
+  }
+  int8_t* const group = a.v + block * (PAGE * D) + w * (D * 16);
+  if (NS == 1 && !old_here) {
+    if (hh == 0) {
+      group[(2 * l) * 16 + (lo & 15)] = int8_t(c[0][0]);
+      group[(2 * l + 1) * 16 + (lo & 15)] = int8_t(c[0][1]);
+    }
+    return;
+  }
+  const bool whole = NS > 1 && lo <= 16 * w && hi >= 16 * w + 16;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint32_t* const at = reinterpret_cast<uint32_t*>(group + (2 * l + e) * 16 + hh * SL);
+    uint32_t words[SL / 4];
+#pragma unroll
+    for (int i = 0; i < SL / 4; ++i) words[i] = whole ? 0u : at[i];  // slots past the new ones keep what they hold
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      const int slot = first_slot + s;
+      const int sh = 8 * (s & 3);
+      const int was = int8_t(words[s >> 2] >> sh);
+      int now = was;
+      if (slot < lo) now = old_here ? rescaled(was, ratio) : was;
+      else if (slot < hi) now = c[NS == 1 ? 0 : s][e];
+      words[s >> 2] = (words[s >> 2] & ~(255u << sh)) | (uint32_t(now & 255) << sh);
+    }
+#pragma unroll
+    for (int i = 0; i < SL / 4; ++i) at[i] = words[i];
+  }
+}
+
+template <bool BF16, int D, int PAGE>
+__global__ __launch_bounds__(PAGE * 4) void cache_append_kernel(AppendArgs a) {
+  constexpr int LPR = D / 2, SL = 16 * LPR / 64, WAVES = PAGE / 16;
+  int64_t id = blockIdx.x;
+  if (id < a.kv_wgs) {
+    const int side = id & 1;
+    id >>= 1;
+    const int head = id % a.kvh;
+    id /= a.kvh;
+    const int j = id % a.blocks, b = id / a.blocks;
+    const Seq s = sequence(a.seq, b, j == 0 && head == 0 && side == 0 && threadIdx.x == 0);
+    if (s.n <= 0) return;
+    const int first = s.len - s.n;  // position of the first new token; below 0: those tokens have no place
+    if (first < 0 && j == 0 && threadIdx.x == 0) report(a.seq.info, KQ_INFO_LENGTH);
+    if ((int64_t(max(first, 0) / PAGE) + j) * PAGE >= s.len) return;
+    const int pos0 = (max(first, 0) / PAGE + j) * PAGE;
+    const int lo = max(max(first, 0) - pos0, 0), hi = min(PAGE, s.len - pos0);
+    const int pageid = page_of(a.seq, b, pos0);
+    if (pageid < 0) return;
+    const int row_lo = s.row0 + pos0 + lo - first;
+    if (hi - lo == 1)
+      append_block<BF16, D, PAGE, 1>(a, side, head, pageid, pos0, lo, hi, row_lo);
+    else
+      append_block<BF16, D, PAGE, SL>(a, side, head, pageid, pos0, lo, hi, row_lo);
+    return;
+  }
+  // queries: a wave for each token and group of heads
+  id -= a.kv_wgs;
+  const int lane = threadIdx.x & 63, l = lane & (LPR - 1), hh = lane / LPR;
+  const int64_t item = id * WAVES + (threadIdx.x >> 6);
+  const int64_t items = int64_t(a.seq.max_q) * a.q_groups;
+  const int64_t per_b = (items + WAVES - 1) / WAVES * WAVES;
+  const int b = item / per_b;
+  const int64_t in = item - b * per_b;
+  if (in >= items) return;
+  const int i = in / a.q_groups, gq = in - int64_t(i) * a.q_groups;
+  const Seq s = sequence(a.seq, b, false);
+  if (i >= s.n) return;
+  const int64_t p = int64_t(s.len) - s.n + i;
+  const bool norm = a.norm[0] != nullptr;
+  const float2 wt = norm ? *reinterpret_cast<const float2*>(a.norm[0] + 2 * l) : make_float2(1.0f, 1.0f);
+  const bool off = p < 0 || (a.rope && p >= a.rope_len);
+  if (off && a.rope && p >= a.rope_len && lane == 0) report(a.seq.info, KQ_INFO_POSITION);
+  const float* cs = a.rope ? a.rope + (off ? 0 : p) * a.rot : nullptr;
+  const int64_t row = s.row0 + i;
+  const int h_per = (a.heads + a.q_groups - 1) / a.q_groups;
+  const int h1 = min(a.heads, (gq + 1) * h_per);
+  constexpr int RW = 64 / LPR;  // heads a wave takes at a time
+  for (int h0 = gq * h_per; h0 < h1; h0 += 4 * RW) {
+    float2 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      x[u] = load2<BF16>(a.src[0], row * a.ld[0] + int64_t(min(h0 + u * RW + hh, h1 - 1)) * D + 2 * l);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (h0 + u * RW >= h1) break;  // uniform
+      double y0 = x[u].x, y1 = x[u].y;
+      place<D>(y0, y1, norm, wt, a.eps, cs, a.rot, a.interleaved, l);
+      if (off) y0 = y1 = NAN;
+      const int h = h0 + u * RW + hh;
+      if (h < h1) {
+        const int64_t at = row * a.ldqo + int64_t(h) * D + 2 * l;
+        // to bf16 through float32: 2^-8 half a step of bf16, 2^-25 more
+        if (BF16)
+          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.q_out) + at) =
+              f32_to_bf16(float(y0)) | (f32_to_bf16(float(y1)) << 16);
+        else
+          *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.q_out) + at) = make_float2(float(y0), float(y1));
+      }
+    }
+  }
+}
+
+template <bool BF16, int D, int PAGE>
+void launch_append(const AppendArgs& a, int64_t wgs, hipStream_t st) {
+  LaunchTimer timer("cache_append_kernel", st);
+  hipLaunchKernelGGL((cache_append_kernel<BF16, D, PAGE>), dim3(static_cast<uint32_t>(wgs)), dim3(PAGE * 4), 0, st, a);
+}
+
+template <bool BF16, int D>
+void launch_append(const AppendArgs& a, int page, int64_t wgs, hipStream_t st) {
+  switch (page) {
+    case 16: launch_append<BF16, D, 16>(a, wgs, st); break;
+    case 32: launch_append<BF16, D, 32>(a, wgs, st); break;
+    case 64: launch_append<BF16, D, 64>(a, wgs, st); break;
+    default: launch_append<BF16, D, 128>(a, wgs, st); break;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// reading back
+// ---------------------------------------------------------------------------
+
+struct ReadArgs {
+  SeqArgs seq;
+  const int8_t* k;
+  const int8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  void* out[2];
+  int64_t ld[2];
+  int kvh;
+  int groups;  // 16-token groups a sequence's rows can touch
+  int64_t items;
+};
+
+// 16 consecutive values at out + at (8 + 8 bf16 or 4 x 4 float32).
+template <bool BF16>
+__device__ __forceinline__ void store16(void* out, int64_t at, uint4 codes, float scale) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) f[t] = float(int8_t(w[i] >> (8 * t))) * scale;
+    if (BF16) {
+      uint2 o;
+      o.x = f32_to_bf16(f[0]) | (f32_to_bf16(f[1]) << 16);
+      o.y = f32_to_bf16(f[2]) | (f32_to_bf16(f[3]) << 16);
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + at + 4 * i) = o;
+    } else {
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at + 4 * i) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+  }
+}
+
+// A wave for each 16 tokens of a head: the keys 16 channels a lane, the values two channels a lane.
+template <bool BF16, int D>
+__global__ __launch_bounds__(256) void cache_read_kernel(ReadArgs a) {
+  const int lane = threadIdx.x & 63;
+  int64_t item = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (item >= a.items) return;
+  const int head = item % a.kvh;
+  item /= a.kvh;
+  const int j = item % a.groups, b = item / a.groups;
+  const Seq s = sequence(a.seq, b, j == 0 && head == 0 && lane == 0);
+  if (s.n <= 0) return;
+  const int first = s.len - s.n;
+  const int page = 1 << a.seq.page_log2;
+  if (first < 0 && j == 0) {
+    if (lane == 0) report(a.seq.info, KQ_INFO_LENGTH);
+    for (int i = 0; i < min(-first, s.n); ++i)  // rows without a place
+      for (int d = lane; d < 2 * D; d += 64) {
+        void* const out = a.out[d / D];
+        const int64_t at = (int64_t(s.row0) + i) * a.ld[d / D] + int64_t(head) * D + d % D;
+        if (!out) continue;
+        if (BF16) reinterpret_cast<uint16_t*>(out)[at] = 0x7fc0;
+        else reinterpret_cast<float*>(out)[at] = NAN;
+      }
+  }
+  if ((int64_t(max(first, 0) / 16) + j) * 16 >= s.len) return;
+  const int pos0 = (max(first, 0) / 16 + j) * 16;
+  const int lo = max(max(first, 0) - pos0, 0), hi = min(16, s.len - pos0);
+  const int id = page_of(a.seq, b, pos0);
+  const int64_t block = int64_t(max(id, 0)) * a.kvh + head;
+  const float ks = id < 0 ? NAN : a.k_scale[block], vs = id < 0 ? NAN : a.v_scale[block];
+  const int off = pos0 & (page - 1);
+  const int64_t row0 = int64_t(s.row0) + pos0 - first;  // row of slot 0 of the group
+  if (a.out[0]) {
+    const int8_t* const src = a.k + (block * page + off) * D;
+    constexpr int LR = D / 16, STEPS = 16 * LR / 64;    // lanes a row
+    uint4 c[STEPS];
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) c[t] = *reinterpret_cast<const uint4*>(src + (64 * t + lane) * 16);
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) {
+      const int slot = (64 * t + lane) / LR, d = (lane % LR) * 16;
+      if (slot >= lo && slot < hi) store16<BF16>(a.out[0], (row0 + slot) * a.ld[0] + int64_t(head) * D + d, c[t], ks);
+    }
+  }
+  if (a.out[1]) {
+    constexpr int LPR = D / 2;
+    const int l = lane & (LPR - 1), hh = lane / LPR;
+    const uint4* const src = reinterpret_cast<const uint4*>(a.v + (block * page + off) * D) + 2 * l;
+    const uint4 c0 = src[0], c1 = src[1];
+    const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      if (D == 64 && (t & 1) != hh) continue;           // two rows at a time
+      if (t < lo || t >= hi) continue;
+      const float f0 = float(int8_t(w0[t >> 2] >> (8 * (t & 3)))) * vs, f1 = float(int8_t(w1[t >> 2] >> (8 * (t & 3)))) * vs;
+      const int64_t at = (row0 + t) * a.ld[1] + int64_t(head) * D + 2 * l;
+      if (BF16)
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out[1]) + at) = f32_to_bf16(f0) | (f32_to_bf16(f1) << 16);
+      else
+        *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out[1]) + at) = make_float2(f0, f1);
+    }
+  }
+}
+
+}  // namespace
+
+kq_status cache_append_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q, CacheIn k, CacheIn v, bool bf16,
+                           int64_t rows, int heads, const float* q_norm, const float* k_norm, float eps,
+                           const float* rope, int64_t rope_len, int rot_dim, bool interleaved, void* q_out,
+                           int64_t ldqo, int32_t* info, hipStream_t st) {
+  AppendArgs a;
+  a.seq = seq_args(c, b, rows, info);
+  a.src[0] = q.p;
+  a.src[1] = k.p;
+  a.src[2] = v.p;
+  a.ld[0] = q.ld;
+  a.ld[1] = k.ld;
+  a.ld[2] = v.ld;
+  a.norm[0] = q_norm;
+  a.norm[1] = k_norm;
+  a.eps = eps;
+  a.rope = rope;
+  a.rope_len = rope_len;
+  a.rot = rot_dim;
+  a.interleaved = interleaved;
+  a.q_out = q_out;
+  a.ldqo = ldqo;
+  a.k = c.k;
+  a.v = c.v;
+  a.k_scale = c.k_scale;
+  a.v_scale = c.v_scale;
+  a.heads = heads;
+  a.kvh = c.kv_heads;
+  a.batch = b.batch;
+  // max_q consecutive tokens touch at most this many blocks, wherever they begin
+  a.blocks = static_cast<int>((int64_t(b.max_q) + c.page - 2) / c.page + 1);
+  a.kv_wgs = int64_t(b.batch) * a.blocks * c.kv_heads * 2;
+  const int waves = c.page / 16;
+  // a wave takes 8 heads of a token; all heads of a few tokens are spread wider, for latency
+  const int per_wave = int64_t(b.batch) * b.max_q * heads > 8192 ? 8 : (c.head_dim == 64 ? 2 : 1);
+  a.q_groups = heads ? (heads + per_wave - 1) / per_wave : 1;
+  const int64_t per_b = (int64_t(b.max_q) * a.q_groups + waves - 1) / waves * waves;
+  const int64_t q_wgs = q_out ? int64_t(b.batch) * per_b / waves : 0;
+  const int64_t wgs = a.kv_wgs + q_wgs;
+  if (wgs > int64_t(INT32_MAX))
+    return fail(KQ_EUNSUPPORTED, "kq_cache_append: batch %d with max_q %d needs too many workgroups", b.batch, b.max_q);
+  if (bf16) {
+    if (c.head_dim == 64) launch_append<true, 64>(a, c.page, wgs, st);
+    else launch_append<true, 128>(a, c.page, wgs, st);
+  } else {
+    if (c.head_dim == 64) launch_append<false, 64>(a, c.page, wgs, st);
+    else launch_append<false, 128>(a, c.page, wgs, st);
+  }
+  return check_launch("cache_append_kernel");
+}
+
+kq_status cache_read_run(const kq_cache& c, const kq_cache_batch& b, void* k_out, void* v_out, bool bf16, int64_t rows,
+                         int64_t ldk, int64_t ldv, int32_t* info, hipStream_t st) {
+  ReadArgs a;
+  a.seq = seq_args(c, b, rows, info);
+  a.k = c.k;
+  a.v = c.v;
+  a.k_scale = c.k_scale;
+  a.v_scale = c.v_scale;
+  a.out[0] = k_out;
+  a.out[1] = v_out;
+  a.ld[0] = ldk;
+  a.ld[1] = ldv;
+  a.kvh = c.kv_heads;
+  a.groups = static_cast<int>((int64_t(b.max_q) + 14) / 16 + 1);
+  a.items = int64_t(b.batch) * a.groups * c.kv_heads;
+  const int64_t wgs = (a.items + 3) / 4;
+  if (wgs > int64_t(INT32_MAX))
+    return fail(KQ_EUNSUPPORTED, "kq_cache_read: batch %d with max_q %d needs too many workgroups", b.batch, b.max_q);
+  {
+    LaunchTimer timer("cache_read_kernel", st);
+    const dim3 grid(static_cast<uint32_t>(wgs)), block(256);
+    if (bf16) {
+      if (c.head_dim == 64) hipLaunchKernelGGL((cache_read_kernel<true, 64>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((cache_read_kernel<true, 128>), grid, block, 0, st, a);
+    } else {
+      if (c.head_dim == 64) hipLaunchKernelGGL((cache_read_kernel<false, 64>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((cache_read_kernel<false, 128>), grid, block, 0, st, a);
+    }
+  }
+  return check_launch("cache_read_kernel");
+}
+
+}  // namespace kq

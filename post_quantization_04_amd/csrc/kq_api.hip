@@ -367,3 +367,123 @@ kq_status kq_decode_matvec(const uint32_t* packed, const float* scales, const ui
 }
 
 }  // extern "C"
+
+namespace {
+
+// The sizes of a cache and a batch (pointers apart, so that the workspace query can use it too).
+kq_status cache_sizes(const char* what, const kq_cache* c, const kq_cache_batch* b, int64_t rows) {
+  if (!c || !b) return fail(KQ_EINVAL, "%s: NULL cache or batch", what);
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128)
+    return fail(KQ_EINVAL, "%s: page must be 16, 32, 64 or 128, got %d", what, c->page);
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return fail(KQ_EUNSUPPORTED, "%s: head_dim must be 64 or 128, got %d", what, c->head_dim);
+  if (c->pages < 1 || c->pages > INT32_MAX || c->kv_heads < 1 || c->kv_heads > 65536)
+    return fail(KQ_EINVAL, "%s: bad cache shape pages=%lld kv_heads=%d", what, (long long)c->pages, c->kv_heads);
+  if (b->batch < 0 || b->max_pages < 1 || b->max_q < 0 || int64_t(b->max_pages) * c->page > INT32_MAX)
+    return fail(KQ_EINVAL, "%s: bad batch shape batch=%d max_pages=%d max_q=%d", what, b->batch, b->max_pages, b->max_q);
+  if (rows < 0 || rows > INT32_MAX) return fail(KQ_EINVAL, "%s: bad row count %lld", what, (long long)rows);
+  return KQ_OK;
+}
+
+kq_status cache_pointers(const char* what, const kq_cache* c, const kq_cache_batch* b) {
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return fail(KQ_EINVAL, "%s: NULL cache pointer", what);
+  if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15)
+    return fail(KQ_EINVAL, "%s: the cache's codes must be 16-byte aligned", what);
+  if (!b->table || !b->seq_lens || !b->q_start) return fail(KQ_EINVAL, "%s: NULL batch pointer", what);
+  return KQ_OK;
+}
+
+// One [rows, heads, head_dim] tensor of a cache call.
+kq_status cache_tensor(const char* what, const char* name, const void* p, int32_t dtype, int64_t rows, int64_t heads,
+                       int64_t dim, int64_t ld) {
+  if (!p && rows > 0) return fail(KQ_EINVAL, "%s: %s is NULL", what, name);
+  if (ld < heads * dim) return fail(KQ_EINVAL, "%s: %s: pitch %lld < %lld", what, name, (long long)ld, (long long)(heads * dim));
+  const int64_t per16 = dtype == KQ_BF16 ? 8 : 4;
+  if ((reinterpret_cast<uintptr_t>(p) & 15) || ld % per16)
+    return fail(KQ_EINVAL, "%s: %s must be 16-byte aligned with a pitch of whole 16 bytes", what, name);
+  return KQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kq_status kq_cache_append(const kq_cache* cache, const kq_cache_batch* batch, const void* q, const void* k,
+                          const void* v, int32_t dtype, int64_t rows, int32_t heads, int64_t ldq, int64_t ldk,
+                          int64_t ldv, const float* q_norm, const float* k_norm, float eps, const float* rope,
+                          int64_t rope_len, int32_t rot_dim, uint32_t flags, void* q_out, int64_t ldqo,
+                          int32_t* info, void* stream) {
+  const char* const what = "kq_cache_append";
+  kq_status st = cache_sizes(what, cache, batch, rows);
+  if (st != KQ_OK) return st;
+  if (dtype != KQ_BF16 && dtype != KQ_F32) return fail(KQ_EINVAL, "%s: dtype must be KQ_BF16 or KQ_F32", what);
+  if (flags & ~uint32_t(KQ_ROPE_INTERLEAVED)) return fail(KQ_EINVAL, "%s: unknown flags %u", what, flags);
+  if ((st = cache_pointers(what, cache, batch)) != KQ_OK) return st;
+  if (!q != !q_out || (q && heads < 1) || heads < 0 || heads > 65536 || (!q && heads != 0))
+    return fail(KQ_EINVAL, "%s: q and q_out come together, with heads >= 1, or both NULL with heads 0", what);
+  if (q) {
+    if ((st = cache_tensor(what, "q", q, dtype, rows, heads, cache->head_dim, ldq)) != KQ_OK) return st;
+    if ((st = cache_tensor(what, "q_out", q_out, dtype, rows, heads, cache->head_dim, ldqo)) != KQ_OK) return st;
+    if (q == q_out && ldq != ldqo) return fail(KQ_EINVAL, "%s: q in place needs equal pitches", what);
+  }
+  if ((st = cache_tensor(what, "k", k, dtype, rows, cache->kv_heads, cache->head_dim, ldk)) != KQ_OK) return st;
+  if ((st = cache_tensor(what, "v", v, dtype, rows, cache->kv_heads, cache->head_dim, ldv)) != KQ_OK) return st;
+  if ((q_norm || k_norm) && !(eps > 0.0f && std::isfinite(eps)))
+    return fail(KQ_EINVAL, "%s: eps must be finite and > 0", what);
+  if (((reinterpret_cast<uintptr_t>(q_norm) | reinterpret_cast<uintptr_t>(k_norm)) & 7))
+    return fail(KQ_EINVAL, "%s: norm weights must be 8-byte aligned", what);
+  if (rope && (rope_len < 1 || rot_dim < 4 || rot_dim % 4 || rot_dim > cache->head_dim))
+    return fail(KQ_EINVAL, "%s: rot_dim must be a multiple of 4 up to head_dim, with rope_len >= 1 (rot_dim %d, rope_len %lld)",
+                what, rot_dim, (long long)rope_len);
+  if (rows == 0 || batch->batch == 0 || batch->max_q == 0) return KQ_OK;
+  return kq::cache_append_run(*cache, *batch, {q, ldq}, {k, ldk}, {v, ldv}, dtype == KQ_BF16, rows, heads, q_norm, k_norm,
+                              eps, rope, rope_len, rot_dim, (flags & KQ_ROPE_INTERLEAVED) != 0, q_out, ldqo, info,
+                              kq::as_stream(stream));
+}
+
+kq_status kq_cache_read(const kq_cache* cache, const kq_cache_batch* batch, void* k_out, void* v_out, int32_t dtype,
+                        int64_t rows, int64_t ldk, int64_t ldv, int32_t* info, void* stream) {
+  const char* const what = "kq_cache_read";
+  kq_status st = cache_sizes(what, cache, batch, rows);
+  if (st != KQ_OK) return st;
+  if (dtype != KQ_BF16 && dtype != KQ_F32) return fail(KQ_EINVAL, "%s: dtype must be KQ_BF16 or KQ_F32", what);
+  if ((st = cache_pointers(what, cache, batch)) != KQ_OK) return st;
+  if (!k_out && !v_out && rows > 0) return fail(KQ_EINVAL, "%s: neither k_out nor v_out", what);
+  if (k_out && (st = cache_tensor(what, "k_out", k_out, dtype, rows, cache->kv_heads, cache->head_dim, ldk)) != KQ_OK) return st;
+  if (v_out && (st = cache_tensor(what, "v_out", v_out, dtype, rows, cache->kv_heads, cache->head_dim, ldv)) != KQ_OK) return st;
+  if (rows == 0 || batch->batch == 0 || batch->max_q == 0) return KQ_OK;
+  return kq::cache_read_run(*cache, *batch, k_out, v_out, dtype == KQ_BF16, rows, ldk, ldv, info, kq::as_stream(stream));
+}
+
+size_t kq_cache_attention_workspace(const kq_cache* cache, const kq_cache_batch* batch, int32_t dtype, int64_t rows,
+                                    int32_t heads, int32_t window) {
+  const size_t bad = static_cast<size_t>(-1);
+  if (cache_sizes("kq_cache_attention_workspace", cache, batch, rows) != KQ_OK) return bad;
+  if ((dtype != KQ_BF16 && dtype != KQ_F32) || heads < 1 || heads > 65536 || heads % cache->kv_heads || window < 0) return bad;
+  if (rows == 0 || batch->batch == 0 || batch->max_q == 0) return 0;
+  return kq::cache_attention_workspace(*cache, *batch, dtype == KQ_BF16, rows, heads, window);
+}
+
+kq_status kq_cache_attention(const kq_cache* cache, const kq_cache_batch* batch, const void* q, int32_t dtype,
+                             int64_t rows, int32_t heads, int64_t ldq, float scale, int32_t window, void* out,
+                             int64_t ldo, int32_t* info, void* ws, size_t ws_bytes, void* stream) {
+  const char* const what = "kq_cache_attention";
+  kq_status st = cache_sizes(what, cache, batch, rows);
+  if (st != KQ_OK) return st;
+  if (dtype != KQ_BF16 && dtype != KQ_F32) return fail(KQ_EINVAL, "%s: dtype must be KQ_BF16 or KQ_F32", what);
+  if ((st = cache_pointers(what, cache, batch)) != KQ_OK) return st;
+  if (heads < 1 || heads > 65536 || heads % cache->kv_heads)
+    return fail(KQ_EINVAL, "%s: heads %d is not a multiple of kv_heads %d", what, heads, cache->kv_heads);
+  if (!(scale > 0.0f && std::isfinite(scale))) return fail(KQ_EINVAL, "%s: scale must be finite and > 0", what);
+  if (window < 0) return fail(KQ_EINVAL, "%s: window %d < 0", what, window);
+  if ((st = cache_tensor(what, "q", q, dtype, rows, heads, cache->head_dim, ldq)) != KQ_OK) return st;
+  if ((st = cache_tensor(what, "out", out, dtype, rows, heads, cache->head_dim, ldo)) != KQ_OK) return st;
+  if (rows > 0 && q == out) return fail(KQ_EINVAL, "%s: out must not be q", what);
+  if (rows == 0 || batch->batch == 0 || batch->max_q == 0) return KQ_OK;
+  if (!ws_ok(ws, ws_bytes, kq::cache_attention_workspace(*cache, *batch, dtype == KQ_BF16, rows, heads, window))) return KQ_EINVAL;
+  if (reinterpret_cast<uintptr_t>(ws) & 15) return fail(KQ_EINVAL, "%s: workspace must be 16-byte aligned", what);
+  return kq::cache_attention_run(*cache, *batch, {q, ldq}, dtype == KQ_BF16, rows, heads, scale, window, out, ldo, info, ws,
+                                 kq::as_stream(stream));
+}
+
+}  // extern "C"

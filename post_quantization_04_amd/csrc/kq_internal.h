@@ -96,4 +96,21 @@ kq_status decode_run(const kq_decode_layer* layers, int n_layers, int64_t din, i
 // once per device and kept); KQ_EDEVICE if the runtime cannot resolve it.
 kq_status decode_static_scratch(void** ptr);
 
+// 8-bit key/value cache (cache.hip) and the attention over it (cache_attn.hip)
+struct CacheIn {            // one tensor argument of the cache calls: [rows, heads, head_dim], row pitch in elements
+  const void* p;
+  int64_t ld;
+};
+kq_status cache_append_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q, CacheIn k, CacheIn v, bool bf16,
+                           int64_t rows, int heads, const float* q_norm, const float* k_norm, float eps,
+                           const float* rope, int64_t rope_len, int rot_dim, bool interleaved, void* q_out,
+                           int64_t ldqo, int32_t* info, hipStream_t st);
+kq_status cache_read_run(const kq_cache& c, const kq_cache_batch& b, void* k_out, void* v_out, bool bf16, int64_t rows,
+                         int64_t ldk, int64_t ldv, int32_t* info, hipStream_t st);
+size_t cache_attention_workspace(const kq_cache& c, const kq_cache_batch& b, bool bf16, int64_t rows, int heads,
+                                 int window);
+kq_status cache_attention_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q, bool bf16, int64_t rows,
+                              int heads, float scale, int window, void* out, int64_t ldo, int32_t* info, void* ws,
+                              hipStream_t st);
+
 }  // namespace kq

@@ -13,8 +13,9 @@ from typing import Optional
 import numpy as np
 
 from . import (KQ_BIIP_INPUT, KQ_BIIP_INVERSE, KQ_BIIP_OUTPUT, KQ_BIIP_SCALE, KQ_SCORE_KRONQ, KQError,
-               KQ_EINVAL, KQ_ENOTPD, Rot, accumulate_cov, accumulate_xcov, biip_rotate, biip_transform,
-               cholesky_inv, gptaq_target, make_rot, obs_quantize, sensitivity)
+               KQ_EINVAL, KQ_ENOTPD, CacheBatch, KVCache, Rot, _need, accumulate_cov, accumulate_xcov, biip_rotate,
+               biip_transform, cache_append, cache_attention, cache_attention_workspace, cholesky_inv,
+               decode_matvec_group, decode_workspace, gptaq_target, make_rot, obs_quantize, sensitivity)
 
 ALL_SIDES = KQ_BIIP_INPUT | KQ_BIIP_OUTPUT | KQ_BIIP_SCALE
 
@@ -130,3 +131,60 @@ def score(h_x, h_g, mode: int = KQ_SCORE_KRONQ, stream=None) -> float:
     s = torch.empty(1, dtype=torch.float64, device=h_x.device)
     sensitivity(h_x, h_g, s, mode, stream=stream)
     return float(s.item())
+
+
+def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device=None):
+    """Rotation table for cache_append: float32 [positions, rot_dim], row p holding cos then sin of
+    p base^(-2j / rot_dim), j < rot_dim / 2, computed in float64 (far positions lose their angle in float32)."""
+    import torch
+    j = torch.arange(rot_dim // 2, dtype=torch.float64, device=device)
+    angle = torch.outer(torch.arange(positions, dtype=torch.float64, device=device), base ** (-2.0 * j / rot_dim))
+    return torch.cat((angle.cos(), angle.sin()), 1).to(torch.float32)
+
+
+def attention_step(x, qkv, o, cache: KVCache, batch: CacheBatch, heads: int, *, bits: int, group: int, s_x, rot_in,
+                   o_s_x, o_rot_in, q_norm=None, k_norm=None, eps: float = 1e-6, rope=None, interleaved: bool = False,
+                   scale: Optional[float] = None, window: int = 0, info=None, ws=None, stream=None):
+    """The attention half of a decoder block on quantized weights, for the new tokens x (float32 [rows, d], at most
+    KQ_DECODE_MAX_TOKENS): q, k and v by one decode group call, norm, rotation and append to the 8-bit cache,
+    attention over it, the o projection.
+
+    ``qkv``: the three layers as decode_matvec_group takes them, (packed, scales, zeros, s_g, rot_out, y), y float32
+    [rows, heads * head_dim] and twice [rows, kv_heads * head_dim]; ``o``: one such layer, din = heads * head_dim.
+    ``s_x`` and ``rot_in`` belong to q, k and v, ``o_s_x`` and ``o_rot_in`` to o. Returns o's y. The values in
+    qkv's q are replaced by the rotated queries. ``ws`` (from ``attention_step_workspace``) and the layers' y make
+    the step free of allocations, so that it can be captured into a graph."""
+    rows, dim = x.shape[0], cache.head_dim
+    y_q, y_k, y_v = (layer[5] for layer in qkv)
+    _need(y_q.shape == (rows, heads * dim) and y_k.shape == y_v.shape == (rows, cache.kv_heads * dim),
+          "attention_step: the layers' y do not match heads, kv_heads and head_dim")
+    if ws is None:
+        ws = attention_step_workspace(x, qkv, o, cache, batch, heads)
+    q = y_q.view(rows, heads, dim)
+    decode_matvec_group(qkv, bits, group, s_x, rot_in, x, ws=ws.qkv, stream=stream)
+    cache_append(cache, batch, q, y_k.view(rows, cache.kv_heads, dim), y_v.view(rows, cache.kv_heads, dim), q,
+                 q_norm=q_norm, k_norm=k_norm, eps=eps, rope=rope, interleaved=interleaved, info=info, stream=stream)
+    cache_attention(cache, batch, q, ws.attn.view(rows, heads, dim), scale=scale, window=window, info=info,
+                    ws=ws.scratch, stream=stream)
+    decode_matvec_group([o], bits, group, o_s_x, o_rot_in, ws.attn, ws=ws.o, stream=stream)
+    return o[5]
+
+
+@dataclass
+class StepWorkspace:
+    """Buffers of attention_step; steps that share them must not overlap."""
+    qkv: object         # decode scratch of the q, k, v call
+    o: object           # and of the o call
+    attn: object        # the attention's output, float32 [rows, heads * head_dim]
+    scratch: object     # cache_attention's workspace
+
+
+def attention_step_workspace(x, qkv, o, cache: KVCache, batch: CacheBatch, heads: int) -> StepWorkspace:
+    """The buffers attention_step needs for inputs like these."""
+    import torch
+    rows, dev = x.shape[0], x.device
+    wide = heads * cache.head_dim
+    attn = torch.empty((rows, wide), dtype=torch.float32, device=dev)
+    return StepWorkspace(decode_workspace(sum(layer[5].shape[1] for layer in qkv), x.shape[1], rows, dev),
+                         decode_workspace(o[5].shape[1], wide, rows, dev), attn,
+                         cache_attention_workspace(cache, batch, attn.view(rows, heads, cache.head_dim)))

@@ -1,0 +1,259 @@
+"""The 8-bit key/value cache without a GPU: refused arguments (before any launch), workspace sizes, the binding's
+own checks, and the oracle on cases whose answer is known."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import post_quantization_04_amd as kq
+from oracle import kvcache
+
+ADDR = 0x10000  # never dereferenced: every call below fails validation, or has nothing to do, first
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+    if not os.path.exists(kq.lib_path()):
+        pytest.skip("libkq.so not built")
+    return kq.lib()
+
+
+def _cache(**kw):
+    f = dict(k=ADDR, v=ADDR, k_scale=ADDR, v_scale=ADDR, pages=10, page=64, kv_heads=8, head_dim=128)
+    f.update(kw)
+    return kq.CacheStruct(*[f[n] for n, _ in kq.CacheStruct._fields_])
+
+
+def _batch(**kw):
+    f = dict(table=ADDR, seq_lens=ADDR, q_start=ADDR, batch=2, max_pages=5, max_q=3)
+    f.update(kw)
+    return kq.CacheBatchStruct(*[f[n] for n, _ in kq.CacheBatchStruct._fields_])
+
+
+BAD_CACHE = [(dict(page=8), kq.KQ_EINVAL), (dict(page=48), kq.KQ_EINVAL), (dict(page=256), kq.KQ_EINVAL),
+             (dict(head_dim=96), kq.KQ_EUNSUPPORTED), (dict(head_dim=0), kq.KQ_EUNSUPPORTED), (dict(pages=0), kq.KQ_EINVAL),
+             (dict(pages=2 ** 31), kq.KQ_EINVAL), (dict(kv_heads=0), kq.KQ_EINVAL), (dict(k=None), kq.KQ_EINVAL),
+             (dict(v=None), kq.KQ_EINVAL), (dict(k_scale=None), kq.KQ_EINVAL), (dict(v_scale=None), kq.KQ_EINVAL),
+             (dict(k=ADDR + 8), kq.KQ_EINVAL), (dict(v=ADDR + 4), kq.KQ_EINVAL)]
+BAD_BATCH = [dict(batch=-1), dict(max_pages=0), dict(max_pages=2 ** 25), dict(max_q=-1), dict(table=None),
+             dict(seq_lens=None), dict(q_start=None)]
+
+# arguments after (cache, batch): q, k, v, dtype, rows, heads, ldq, ldk, ldv, q_norm, k_norm, eps, rope, rope_len,
+# rot_dim, flags, q_out, ldqo, info, stream
+APPEND = [ADDR, ADDR, ADDR, kq.KQ_BF16, 4, 32, 4096, 1024, 1024, None, None, 1e-6, ADDR, 100, 128, 0, ADDR, 4096, None, None]
+# q, dtype, rows, heads, ldq, scale, window, out, ldo, info, ws, ws_bytes, stream
+ATTEND = [ADDR, kq.KQ_F32, 4, 32, 4096, 0.1, 0, ADDR + 16, 4096, None, ADDR, 1 << 40, None]
+# k_out, v_out, dtype, rows, ldk, ldv, info, stream
+READ = [ADDR, ADDR, kq.KQ_F32, 4, 1024, 1024, None, None]
+
+
+def _with(args, at, value):
+    out = list(args)
+    out[at] = value
+    return out
+
+
+def _calls(L):
+    return [(L.kq_cache_append, APPEND), (L.kq_cache_attention, ATTEND), (L.kq_cache_read, READ)]
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHE)
+def test_bad_cache(L, bad, status):
+    for fn, args in _calls(L):
+        assert fn(ctypes.byref(_cache(**bad)), ctypes.byref(_batch()), *args) == status
+        assert L.kq_last_error()
+
+
+@pytest.mark.parametrize("bad", BAD_BATCH)
+def test_bad_batch(L, bad):
+    for fn, args in _calls(L):
+        assert fn(ctypes.byref(_cache()), ctypes.byref(_batch(**bad)), *args) == kq.KQ_EINVAL
+
+
+def test_null_structs(L):
+    for fn, args in _calls(L):
+        assert fn(None, ctypes.byref(_batch()), *args) == kq.KQ_EINVAL
+        assert fn(ctypes.byref(_cache()), None, *args) == kq.KQ_EINVAL
+
+
+@pytest.mark.parametrize("at,value", [
+    (0, None), (0, ADDR + 2), (1, None), (1, ADDR + 8), (2, None), (2, ADDR + 1), (3, kq.KQ_F64), (3, 7), (4, -1),
+    (4, 2 ** 31), (5, 0), (5, -3), (6, 4095), (6, 4097), (7, 1023), (7, 1028), (8, 1000), (13, 0), (14, 2), (14, 126),
+    (14, 132), (15, 2), (16, None), (16, ADDR + 4), (17, 4098), (17, 4104)])
+def test_append_refusals(L, at, value):
+    # the last entry: in place (q == q_out) with another pitch
+    assert L.kq_cache_append(ctypes.byref(_cache()), ctypes.byref(_batch()), *_with(APPEND, at, value)) == kq.KQ_EINVAL
+    assert L.kq_last_error()
+
+
+@pytest.mark.parametrize("eps", [0.0, -1.0, float("nan"), float("inf")])
+def test_append_norm_needs_eps(L, eps):
+    for at in (9, 10):
+        args = _with(_with(APPEND, at, ADDR), 11, eps)
+        assert L.kq_cache_append(ctypes.byref(_cache()), ctypes.byref(_batch()), *args) == kq.KQ_EINVAL
+
+
+@pytest.mark.parametrize("at,value", [
+    (0, None), (0, ADDR + 8), (1, kq.KQ_F64), (2, -1), (2, 2 ** 31), (3, 0), (3, 12), (4, 4092), (4, 4098), (5, 0.0),
+    (5, -1.0), (5, float("nan")), (5, float("inf")), (6, -1), (7, None), (7, ADDR), (7, ADDR + 20), (8, 100),
+    (10, ADDR + 8)])
+def test_attention_refusals(L, at, value):
+    # (7, ADDR): out is q
+    assert L.kq_cache_attention(ctypes.byref(_cache()), ctypes.byref(_batch()), *_with(ATTEND, at, value)) == kq.KQ_EINVAL
+
+
+def test_attention_small_workspace(L):
+    cache, batch = _cache(), _batch(max_pages=2000)
+    need = L.kq_cache_attention_workspace(ctypes.byref(cache), ctypes.byref(batch), kq.KQ_F32, 4, 32, 0)
+    assert need > 0
+    args = _with(ATTEND, 11, need - 1)
+    assert L.kq_cache_attention(ctypes.byref(cache), ctypes.byref(batch), *args) == kq.KQ_EINVAL
+    assert b"workspace" in L.kq_last_error()
+    assert L.kq_cache_attention(ctypes.byref(cache), ctypes.byref(batch), *_with(ATTEND, 10, None)) == kq.KQ_EINVAL
+
+
+def test_workspace_sizes(L):
+    w = lambda c, b, d=kq.KQ_F32, rows=4, heads=32, window=0: L.kq_cache_attention_workspace(  # noqa: E731
+        ctypes.byref(c), ctypes.byref(b), d, rows, heads, window)
+    bad = ctypes.c_size_t(-1).value
+    assert w(_cache(page=8), _batch()) == bad and w(_cache(), _batch(max_q=-1)) == bad
+    assert w(_cache(), _batch(), d=kq.KQ_F64) == bad and w(_cache(), _batch(), heads=12) == bad
+    assert w(_cache(), _batch(), window=-1) == bad
+    assert w(_cache(), _batch(), rows=0) == 0 and w(_cache(), _batch(max_q=0)) == 0
+    # what window 0 needs is enough for every window
+    for pages in (1, 7, 300, 9000):
+        for max_q in (1, 3, 70, 5000):
+            full = w(_cache(), _batch(max_pages=pages, max_q=max_q), rows=max_q + 3)
+            for window in (1, 100, 4096, 2 ** 31 - 1):
+                assert w(_cache(), _batch(max_pages=pages, max_q=max_q), rows=max_q + 3, window=window) <= full
+
+
+@pytest.mark.parametrize("at,value", [(0, ADDR + 8), (1, ADDR + 2), (2, 5), (3, -2), (4, 1020), (4, 1026), (5, 8)])
+def test_read_refusals(L, at, value):
+    assert L.kq_cache_read(ctypes.byref(_cache()), ctypes.byref(_batch()), *_with(READ, at, value)) == kq.KQ_EINVAL
+
+
+def test_read_needs_an_output(L):
+    assert L.kq_cache_read(ctypes.byref(_cache()), ctypes.byref(_batch()), None, None, *READ[2:]) == kq.KQ_EINVAL
+
+
+def test_nothing_to_do_is_ok(L):
+    for fn, args, rows in ((L.kq_cache_append, APPEND, 4), (L.kq_cache_attention, ATTEND, 2), (L.kq_cache_read, READ, 3)):
+        assert fn(ctypes.byref(_cache()), ctypes.byref(_batch()), *_with(args, rows, 0)) == kq.KQ_OK
+        assert fn(ctypes.byref(_cache()), ctypes.byref(_batch(batch=0)), *args) == kq.KQ_OK
+        assert fn(ctypes.byref(_cache()), ctypes.byref(_batch(max_q=0)), *args) == kq.KQ_OK
+
+
+# ---- the binding's checks --------------------------------------------------------------------------------------
+
+
+def _tensors(rows=3, heads=4, kv_heads=2, dim=64, page=16, pages=6):
+    import torch
+    cache = kq.KVCache.allocate(pages, page, kv_heads, dim, "cpu")
+    batch = kq.CacheBatch(torch.zeros((2, 3), dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
+                          torch.zeros(3, dtype=torch.int32), 2)
+    return cache, batch, torch.zeros((rows, heads, dim)), torch.zeros((rows, kv_heads, dim)), torch.zeros((rows, kv_heads, dim))
+
+
+def test_binding_refuses_cpu_tensors(L):
+    cache, batch, q, k, v = _tensors()
+    for call in (lambda: kq.cache_append(cache, batch, q, k, v, q), lambda: kq.cache_read(cache, batch, k, v),
+                 lambda: kq.cache_attention(cache, batch, q, q.clone())):
+        with pytest.raises(kq.KQError) as e:
+            call()
+        assert e.value.status == kq.KQ_EINVAL
+
+
+def test_binding_shape_and_type_checks(L):
+    import torch
+    cache, batch, q, k, v = _tensors()
+    i32 = dict(dtype=torch.int32)
+    bad = [
+        lambda: kq.KVCache(cache.k, cache.v[:, :, :, :32], cache.k_scale, cache.v_scale),
+        lambda: kq.KVCache(cache.k.float(), cache.v, cache.k_scale, cache.v_scale),
+        lambda: kq.KVCache(cache.k, cache.v, cache.k_scale[:2], cache.v_scale),
+        lambda: kq.KVCache(cache.k[::2], cache.v[::2], cache.k_scale[::2], cache.v_scale[::2]),
+        lambda: kq.KVCache.allocate(3, 24, 2, 64, "cpu"),
+        lambda: kq.CacheBatch(torch.zeros((2, 3), **i32), torch.zeros(3, **i32), torch.zeros(3, **i32), 1),
+        lambda: kq.CacheBatch(torch.zeros((2, 3), **i32), torch.zeros(2, **i32), torch.zeros(2, **i32), 1),
+        lambda: kq.CacheBatch(torch.zeros((2, 3)), torch.zeros(2, **i32), torch.zeros(3, **i32), 1),
+        lambda: kq.CacheBatch(torch.zeros((3, 2), **i32).t(), torch.zeros(2, **i32), torch.zeros(3, **i32), 1),
+        lambda: kq.CacheBatch(torch.zeros((2, 3), **i32), torch.zeros(2, **i32), torch.zeros(3, **i32), -1),
+        lambda: kq.cache_append(cache, batch, q, k[:, :1], v, q),
+        lambda: kq.cache_append(cache, batch, q, k, v[:2], q),
+        lambda: kq.cache_append(cache, batch, q, k, v, None),
+        lambda: kq.cache_append(cache, batch, q.half(), k.half(), v.half(), q.half()),
+        lambda: kq.cache_append(cache, batch, q.bfloat16(), k, v, q.bfloat16()),
+        lambda: kq.cache_append(cache, batch, q, k.transpose(0, 1).contiguous().transpose(0, 1), v, q),
+        lambda: kq.cache_append(cache, batch, q, k, v, q, q_norm=torch.ones(32)),
+        lambda: kq.cache_append(cache, batch, q, k, v, q, rope=torch.ones(8, 64).double()),
+        lambda: kq.cache_read(cache, batch, None, None),
+        lambda: kq.cache_read(cache, batch, k, v.bfloat16()),
+        lambda: kq.cache_attention(cache, batch, q, q[:2]),
+        lambda: kq.cache_attention(cache, batch, q[0], q[0]),
+        lambda: kq.cache_attention(cache, batch, q, torch.zeros_like(q), ws=torch.zeros(8)),
+        lambda: kq.cache_attention(cache, batch, q, torch.zeros_like(q), info=torch.zeros(1)),
+    ]
+    for n, call in enumerate(bad):
+        with pytest.raises(kq.KQError) as e:
+            call()
+        assert e.value.status == kq.KQ_EINVAL, n
+
+
+# ---- the oracle --------------------------------------------------------------------------------------------------
+
+
+def test_rope_table_and_rotation():
+    from post_quantization_04_amd import pipeline
+    t = pipeline.rope_table(70000, 8).numpy()
+    assert t.shape == (70000, 8) and t.dtype == np.float32
+    p, j = 69999, 3
+    angle = np.float64(p) * 10000.0 ** (-2.0 * j / 8)
+    assert t[p, j] == np.float32(np.cos(angle)) and t[p, 4 + j] == np.float32(np.sin(angle))
+    rng = np.random.default_rng(0)
+    for inter in (False, True):
+        x, y = rng.standard_normal(12), rng.standard_normal(12)
+        # a rotation keeps lengths, leaves what is past rot_dim, and products depend on the distance alone
+        r = [kvcache.norm_rotate(x, None, 0, t[k], 8, inter) for k in (5, 9)]
+        s = [kvcache.norm_rotate(y, None, 0, t[k], 8, inter) for k in (7, 11)]
+        assert np.isclose(np.linalg.norm(r[0]), np.linalg.norm(x), rtol=1e-6)
+        np.testing.assert_array_equal(r[0][8:], x[8:])
+        np.testing.assert_allclose(r[0] @ s[0], r[1] @ s[1], rtol=0, atol=1e-5)
+
+
+def test_block_scale_and_codes():
+    y = np.array([[127.0, -63.5, 0.5, 1.5], [2.5, -0.5, 0.0, -127.0]])
+    s, c, ratio = kvcache.quantize_block(y, np.float32(0))
+    assert s == 1.0 and ratio == 1.0
+    np.testing.assert_array_equal(c, [[127, -64, 0, 2], [2, 0, 0, -127]])  # halves to even
+    s, c, ratio = kvcache.quantize_block(y, np.float32(2.0))
+    assert s == 2.0 and ratio == 1.0 and c[0, 0] == 64 and c[1, 3] == -64
+    s, c, ratio = kvcache.quantize_block(y, np.float32(0.25))
+    assert s == 1.0 and ratio == 0.25
+    s, c, _ = kvcache.quantize_block(np.zeros((1, 4)), np.float32(0))
+    assert s == 0.0 and not c.any()
+    s, c, _ = kvcache.quantize_block(np.full((1, 4), 1e-40), np.float32(0))
+    assert s == kvcache.SCALE_FLOOR and not c.any()
+    assert np.isnan(kvcache.quantize_block(np.array([[np.inf]]), np.float32(1))[0])
+    assert np.isnan(kvcache.quantize_block(np.array([[1.0]]), np.float32(np.nan))[0])
+
+
+def test_oracle_attention_known_answers():
+    cache = kvcache.Cache.zeros(4, 16, 1, 64)
+    rng = np.random.default_rng(1)
+    v = rng.standard_normal((20, 1, 64))
+    table, rope = [[2, 0]], None
+    kvcache.append(cache, table, [20], [0, 20], None, np.zeros((20, 1, 64)), v, rope=rope)
+    got = kvcache.tokens(cache, table[0], 0, 20)[1]
+    assert np.max(np.abs(got - v)) <= 0.5 * np.max(np.abs(v)) / 127 * (1 + 1e-6)
+    # keys of zero: every visible token weighs the same
+    out, _, _, _ = kvcache.attention(cache, table, [20], [0, 2], rng.standard_normal((2, 2, 64)), 0.125)
+    np.testing.assert_allclose(out[1, 0], got[:, 0].mean(0), rtol=1e-12)
+    np.testing.assert_allclose(out[0, 1], got[:19, 0].mean(0), rtol=1e-12)
+    out, _, _, _ = kvcache.attention(cache, table, [20], [0, 1], rng.standard_normal((1, 2, 64)), 0.125, window=3)
+    np.testing.assert_allclose(out[0, 0], got[17:, 0].mean(0), rtol=1e-12)
+    # more rows than tokens: the first ones see nothing
+    out, _, _, _ = kvcache.attention(cache, table, [1], [0, 3], rng.standard_normal((3, 1, 64)), 0.125)
+    assert not out[:2].any()
+    np.testing.assert_allclose(out[2, 0], got[0, 0], rtol=1e-12)
