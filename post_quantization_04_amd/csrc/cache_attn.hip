@@ -28,7 +28,7 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 
 constexpr float kNoToken = -1.0e30f;   // running maximum before the first token (finite: no inf - inf)
 constexpr float kZeroScale = -48.0f;   // log2 taken for a value scale of 0: any finite one (its codes are 0)
-constexpr int kWeightExp = 14;         // weights go to float16 times 2^14
+constexpr float kWeightExp = 14.0f;    // weights are held times 2^14, so that float16 keeps small ones
 
 struct AttnArgs {
   SeqArgs seq;
@@ -44,8 +44,8 @@ struct AttnArgs {
   float scale_log2e;
   int window;
   int batch, tiles, splits;
-  float* part_o;    // [rows * heads][splits][D], weights' sum times codes (times 2^14)
-  float* part_ml;   // [rows * heads][splits][2]: m, sum of w / s_v
+  float* part_o;    // [rows * heads][splits][D], sum of weights (times 2^14) times codes
+  float* part_ml;   // [rows * heads][splits][2]: m, sum of weights (times 2^14) / s_v
 };
 
 // Four signed bytes to two pairs of float16: bytes b + 128 become the low byte of float16 1024 + b + 128.
@@ -135,7 +135,7 @@ __device__ __forceinline__ Range chunk_range(const Seq& s, int i_first, int i_la
 // bytes a lane.
 // ---------------------------------------------------------------------------
 template <bool BF16, int D>
-__global__ __launch_bounds__(256) void cache_token_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void cache_token_kernel(AttnArgs a) {
   constexpr int U = D / 64;       // 16-byte key loads a lane and token row
   constexpr int DT = D / 16;      // 16-channel tiles of the output
   constexpr int PITCH = D + 4;
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(256) void cache_token_kernel(AttnArgs a) {
     l *= fall;
 #pragma unroll
     for (int t = 0; t < DT; ++t) o[t] *= fall;
-    const float shift = lv - m;
+    const float shift = lv - m + kWeightExp;
     float sum = 0.0f;
     float w[16];
 #pragma unroll
@@ -265,10 +265,9 @@ __global__ __launch_bounds__(256) void cache_token_kernel(AttnArgs a) {
     half8 ph[2], pl[2];
 #pragma unroll
     for (int x = 0; x < 16; ++x) {
-      const float y = w[x] * float(1 << kWeightExp);
-      const _Float16 h = _Float16(y);
+      const _Float16 h = _Float16(w[x]);
       ph[x >> 3][x & 7] = h;
-      if (!BF16) pl[x >> 3][x & 7] = _Float16(y - float(h));
+      if (!BF16) pl[x >> 3][x & 7] = _Float16(w[x] - float(h));
     }
 #pragma unroll
     for (int t = 0; t < DT; ++t) {
@@ -311,7 +310,7 @@ __global__ __launch_bounds__(256) void cache_token_kernel(AttnArgs a) {
 #pragma unroll
     for (int w = 0; w < 4; ++w) x += fw[w] * *reinterpret_cast<const floatx4*>(&sh_o[w][q * PITCH + d]);
     if (a.splits == 1) {
-      const float inv = lj == 0.0f ? 0.0f : ldexpf(1.0f / lj, -kWeightExp);
+      const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
       store4<BF16>(a.out, row * a.ldo + int64_t(head) * D + d, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
     } else {
       *reinterpret_cast<floatx4*>(a.part_o + ((row * a.heads + head) * a.splits + split) * D + d) = x;
@@ -319,6 +318,275 @@ __global__ __launch_bounds__(256) void cache_token_kernel(AttnArgs a) {
   }
   if (a.splits > 1 && d0 == 0)
     *reinterpret_cast<float2*>(a.part_ml + ((row * a.heads + head) * a.splits + split) * 2) = make_float2(mj, lj);
+}
+
+// ---------------------------------------------------------------------------
+// Prompts
+// ---------------------------------------------------------------------------
+
+// A block's scales as the weights use them. A NaN (a poisoned block, a bad page) becomes a finite
+// stand-in and `bad`: the rows that see such a block are made NaN apart.
+struct BlockScale {
+  float ks, lv, iv, bad;
+};
+
+__device__ __forceinline__ BlockScale block_scale(float ks, float vs) {
+  BlockScale r;
+  r.bad = ks == ks && vs == vs ? 0.0f : 1.0f;
+  r.ks = ks > 0.0f ? ks : 1.0f;                 // 0: the codes are 0, so any factor will do
+  r.lv = vs > 0.0f ? __log2f(vs) : kZeroScale;
+  r.iv = vs > 0.0f ? 1.0f / vs : 0x1p48f;
+  return r;
+}
+
+template <bool BF16, int D, int NQ, int W>
+__global__ __launch_bounds__(W * 64, NQ == 1 ? 2 : 1) void cache_prompt_kernel(AttnArgs a) {
+  typedef float floatx16 __attribute__((ext_vector_type(16)));
+  constexpr int NT = W * 64, ROWS = 32 * NQ * W;
+  constexpr int KS = D / 16, DT = D / 32;        // MFMA steps over channels, 32-channel output tiles
+  constexpr int KU = D / 8;                      // 16-byte units of a key row in LDS
+  constexpr int CH = 8 * D / NT;                 // 16-byte chunks of codes a thread stages (keys, then values)
+  constexpr int P = BF16 ? 1 : 2;                // float16 pieces of a query and a weight
+  __shared__ half8 sk[2][64 * KU];               // keys: token rows of KU units
+  __shared__ half8 sv[2][D * 8];                 // values: channel rows of 64 tokens
+  __shared__ BlockScale sc[2][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lq = lane & 31, lh = lane >> 5;
+  int64_t id = blockIdx.x;
+  const int nbh = a.batch * a.kvh;
+  const int bh = id % nbh;
+  id /= nbh;
+  const int tile = a.tiles - 1 - int(id % a.tiles), split = id / a.tiles;   // the longest first
+  const int b = bh / a.kvh, kh = bh - b * a.kvh;
+  const Seq s = sequence(a.seq, b, kh == 0 && tile == 0 && split == 0 && tid == 0);
+  const int nrows = s.n * a.g;
+  if (tile * ROWS >= nrows) return;
+  const int first = s.len - s.n;
+  const Range rg = chunk_range(s, tile * ROWS / a.g, (min(tile * ROWS + ROWS, nrows) - 1) / a.g, a.window, split, a.splits);
+
+  // this wave's rows
+  const int w0 = tile * ROWS + wave * 32 * NQ;
+  const int wlast = min(w0 + 32 * NQ, nrows) - 1;
+  const int p_hi = wlast >= w0 ? first + wlast / a.g : -1, p_lo = first + min(w0, nrows - 1) / a.g;
+  half8 qf[P][NQ][KS];
+  float fq[NQ];
+  int pos[NQ];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const int r = min(w0 + 32 * n + lq, nrows - 1);
+    const int i = r / a.g, hd = kh * a.g + (r - i * a.g);
+    pos[n] = first + i;
+    const int64_t at = (int64_t(s.row0) + i) * a.ldq + int64_t(hd) * D + 8 * lh;
+    float amax = 0.0f;
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      float x[8];
+      load8<BF16>(a.q, at + 16 * t, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]) < INFINITY ? fabsf(x[j]) : INFINITY);
+    }
+    amax = fmaxf(amax, __shfl_xor(amax, 32));
+    float up, down;
+    row_scale(amax, up, down);
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      float x[8];
+      load8<BF16>(a.q, at + 16 * t, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float y = x[j] * up;
+        const _Float16 h = _Float16(y);
+        qf[0][n][t][j] = h;
+        if (!BF16) qf[P - 1][n][t][j] = _Float16(y - float(h));
+      }
+    }
+    fq[n] = a.scale_log2e * down;
+  }
+
+  // staging: chunk x < 4 D of keys (token x / (D / 16), 16 channels), then of values (group, channel);
+  // a wave's chunks are all of one 16-token group
+  uint4 raw[CH];
+  float2 rscale;
+  const int page = 1 << a.seq.page_log2;
+  auto group_of = [&](int i) {
+    return ((wave * 64 + NT * i) & (4 * D - 1)) / D;       // 16 tokens are D chunks of either side
+  };
+  auto fetch = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int g = min(max(4 * c + group_of(i), rg.g0), rg.g1);
+      const int pg = max(page_of(a.seq, b, g << 4), 0);
+      const int x = tid + NT * i, y = x & (D - 1);
+      const int64_t at = ((int64_t(pg) * a.kvh + kh) * page + ((g << 4) & (page - 1))) * D + 16 * y;
+      raw[i] = *reinterpret_cast<const uint4*>((wave * 64 + NT * i < 4 * D ? a.k : a.v) + at);
+    }
+    if (tid < 4) {
+      const int g = min(max(4 * c + tid, rg.g0), rg.g1);
+      const int pg = page_of(a.seq, b, g << 4);
+      const int64_t at = int64_t(max(pg, 0)) * a.kvh + kh;
+      rscale = pg < 0 ? make_float2(NAN, NAN) : make_float2(a.k_scale[at], a.v_scale[at]);
+    }
+  };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int x = tid + NT * i, y = x & (4 * D - 1);
+      const half8 h0 = unpack8(raw[i].x, raw[i].y), h1 = unpack8(raw[i].z, raw[i].w);
+      if (wave * 64 + NT * i < 4 * D) {
+        const int tok = y / (D / 16), u = 2 * (y % (D / 16));
+        const int z = (tok & 3) | ((tok >> 2) & 4);
+        sk[buf][tok * KU + (u ^ z)] = h0;
+        sk[buf][tok * KU + ((u + 1) ^ z)] = h1;
+      } else {
+        const int grp = y / D, d = y % D;
+        sv[buf][d * 8 + ((2 * grp) ^ (d & 7))] = h0;
+        sv[buf][d * 8 + ((2 * grp + 1) ^ (d & 7))] = h1;
+      }
+    }
+    if (tid < 4) sc[buf][tid] = block_scale(rscale.x, rscale.y);
+  };
+
+  floatx16 o[NQ][DT];
+  float m[NQ], l[NQ];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    m[n] = kNoToken;
+    l[n] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[n][t][x] = 0.0f;
+  }
+  // token of this lane's key row in a 32-token block, and its bank swizzle
+  const int ktok = 16 * ((lq >> 2) & 1) + 4 * (lq >> 3) + (lq & 3);
+  const int kz = (ktok & 3) | ((ktok >> 2) & 4);
+
+  if (rg.c0 < rg.c1) {
+    fetch(rg.c0);
+    stage(0);
+    fetch(rg.c0 + 1);
+  }
+  __syncthreads();
+  for (int c = rg.c0; c < rg.c1; ++c) {
+    const int buf = (c - rg.c0) & 1;
+    stage(buf ^ 1);
+    fetch(c + 2);
+    const bool active = 64 * c <= p_hi && (a.window <= 0 || 64 * c + 63 > p_lo - a.window);
+    if (active) {
+      floatx16 e[NQ][2];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) e[n][h][x] = 0.0f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < KS; ++t) {
+          const half8 kf = sk[buf][(32 * h + ktok) * KU + ((2 * t + lh) ^ kz)];
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int q = 0; q < P; ++q) e[n][h] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[q][n][t], e[n][h], 0, 0, 0);
+        }
+      const BlockScale b0 = sc[buf][lh], b1 = sc[buf][2 + lh];
+      const bool cut = 64 * c + 63 > p_lo || (a.window > 0 && 64 * c <= p_hi - a.window);
+      half8 pf[P][NQ][4];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        // tokens x of half h are 64 c + 32 h + 16 lh + x
+        const int hi = pos[n] - (64 * c + 16 * lh), lo = a.window > 0 ? hi - a.window : -(1 << 30);
+        if (cut) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) e[n][h][x] = (32 * h + x <= hi && 32 * h + x > lo) ? e[n][h][x] : -INFINITY;
+        }
+        float f0 = b0.ks * fq[n], f1 = b1.ks * fq[n];
+        f0 = f0 < 1e-37f ? 1e-37f : f0;          // above 0, so that a hidden score stays -inf (a NaN stays NaN)
+        f1 = f1 < 1e-37f ? 1e-37f : f1;
+        float x0 = e[n][0][0], x1 = e[n][1][0];
+#pragma unroll
+        for (int x = 1; x < 16; ++x) {
+          x0 = fmaxf(x0, e[n][0][x]);
+          x1 = fmaxf(x1, e[n][1][x]);
+        }
+        float mx = fmaxf(fmaf(x0, f0, b0.lv), fmaf(x1, f1, b1.lv));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        if (__any(mx > m[n])) {
+          const float mn = fmaxf(m[n], mx), fall = exp2_raw(m[n] - mn);
+          m[n] = mn;
+          l[n] *= fall;
+#pragma unroll
+          for (int t = 0; t < DT; ++t) o[n][t] *= fall;
+        }
+        const float s0 = b0.lv - m[n] + kWeightExp, s1 = b1.lv - m[n] + kWeightExp;
+        float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const float w_0 = exp2_raw(fmaf(e[n][0][x], f0, s0)), w_1 = exp2_raw(fmaf(e[n][1][x], f1, s1));
+          sum0 += w_0;
+          sum1 += w_1;
+          const _Float16 h_0 = _Float16(w_0), h_1 = _Float16(w_1);
+          pf[0][n][x >> 3][x & 7] = h_0;
+          pf[0][n][2 + (x >> 3)][x & 7] = h_1;
+          if (!BF16) {
+            pf[P - 1][n][x >> 3][x & 7] = _Float16(w_0 - float(h_0));
+            pf[P - 1][n][2 + (x >> 3)][x & 7] = _Float16(w_1 - float(h_1));
+          }
+        }
+        l[n] += sum0 * b0.iv + sum1 * b1.iv;
+        if (__any((b0.bad != 0.0f) | (b1.bad != 0.0f))) {   // rows that see a poisoned block
+          if ((b0.bad != 0.0f && hi >= 0 && lo < 15) || (b1.bad != 0.0f && hi >= 32 && lo < 47)) l[n] = NAN;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {             // 32-token half k >> 1, its step k & 1
+          const half8 vf = sv[buf][(32 * t + lq) * 8 + ((4 * (k >> 1) + 2 * lh + (k & 1)) ^ (lq & 7))];
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int q = 0; q < P; ++q) o[n][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[q][n][k], o[n][t], 0, 0, 0);
+        }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const int r = w0 + 32 * n + lq;
+    l[n] += __shfl_xor(l[n], 32);
+    if (r >= nrows) continue;
+    const int i = r / a.g, head = kh * a.g + (r - i * a.g);
+    const int64_t row = int64_t(s.row0) + i;
+    if (pos[n] < 0) {                             // sees nothing, whatever its query holds
+      l[n] = 0.0f;
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[n][t][x] = 0.0f;
+    }
+    if (a.splits == 1) {
+      const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          store4<BF16>(a.out, row * a.ldo + int64_t(head) * D + 32 * t + 8 * x + 4 * lh, o[n][t][4 * x] * inv,
+                       o[n][t][4 * x + 1] * inv, o[n][t][4 * x + 2] * inv, o[n][t][4 * x + 3] * inv);
+    } else {
+      const int64_t at = (row * a.heads + head) * a.splits + split;
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          *reinterpret_cast<floatx4*>(a.part_o + at * D + 32 * t + 8 * x + 4 * lh) =
+              floatx4{o[n][t][4 * x], o[n][t][4 * x + 1], o[n][t][4 * x + 2], o[n][t][4 * x + 3]};
+      if (lh == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m[n], l[n]);
+    }
+  }
 }
 
 // Joins the splits of each row: a workgroup for each (sequence, token, head), 256 threads as
@@ -358,37 +626,46 @@ __global__ __launch_bounds__(256) void cache_join_kernel(AttnArgs a) {
     acc += sh[x][threadIdx.x];
     l += sh_l[x];
   }
-  const float inv = l == 0.0f ? 0.0f : ldexpf(1.0f / l, -kWeightExp);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   store4<BF16>(a.out, row * a.ldo + int64_t(head) * D + d, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
 }
 
 struct Plan {
+  bool prompt;
   int tiles, splits;
 };
 
-Plan plan(const kq_cache& c, const kq_cache_batch& b, int heads, int window) {
+Plan plan(const kq_cache& c, const kq_cache_batch& b, bool bf16, int heads, int window) {
   Plan p;
-  const int64_t g = heads / c.kv_heads;
-  p.tiles = static_cast<int>((b.max_q * g + 15) / 16);
+  const int64_t rows = int64_t(b.max_q) * (heads / c.kv_heads);
+  p.prompt = rows > 32;
+  const int rows_wg = p.prompt ? 256 : 16;
+  p.tiles = static_cast<int>((rows + rows_wg - 1) / rows_wg);
   int64_t longest = int64_t(b.max_pages) * c.page;
   if (window > 0) longest = std::min<int64_t>(longest, int64_t(window) + b.max_q + 63);
   const int64_t wgs = int64_t(b.batch) * c.kv_heads * p.tiles;
-  const int64_t want = (4 * kCus + wgs - 1) / wgs;                 // four workgroups a CU
+  const int64_t want = ((p.prompt ? 1 : 4) * kCus + wgs - 1) / wgs;
   p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, (longest + 511) / 512)));
   return p;
 }
 
 template <bool BF16, int D>
-kq_status launch(const AttnArgs& a, hipStream_t st) {
+kq_status launch(const AttnArgs& a, bool prompt, hipStream_t st) {
   const int64_t wgs = int64_t(a.batch) * a.kvh * a.tiles * a.splits;
   const int64_t joins = int64_t(a.batch) * a.seq.max_q * a.heads;
   if (wgs > int64_t(INT32_MAX) || (a.splits > 1 && joins > int64_t(INT32_MAX)))
     return fail(KQ_EUNSUPPORTED, "kq_cache_attention: too many workgroups (batch %d, max_q %d)", a.batch, a.seq.max_q);
-  {
+  const dim3 grid(static_cast<uint32_t>(wgs));
+  kq_status r;
+  if (prompt) {
+    LaunchTimer timer("cache_prompt_kernel", st);
+    hipLaunchKernelGGL((cache_prompt_kernel<BF16, D, 1, 8>), grid, dim3(512), 0, st, a);
+    r = check_launch("cache_prompt_kernel");
+  } else {
     LaunchTimer timer("cache_token_kernel", st);
-    hipLaunchKernelGGL((cache_token_kernel<BF16, D>), dim3(static_cast<uint32_t>(wgs)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((cache_token_kernel<BF16, D>), grid, dim3(256), 0, st, a);
+    r = check_launch("cache_token_kernel");
   }
-  kq_status r = check_launch("cache_token_kernel");
   if (r != KQ_OK || a.splits == 1) return r;
   {
     LaunchTimer timer("cache_join_kernel", st);
@@ -401,8 +678,7 @@ kq_status launch(const AttnArgs& a, hipStream_t st) {
 
 size_t cache_attention_workspace(const kq_cache& c, const kq_cache_batch& b, bool bf16, int64_t rows, int heads,
                                  int window) {
-  (void)bf16;
-  const Plan p = plan(c, b, heads, window);
+  const Plan p = plan(c, b, bf16, heads, window);
   if (p.splits == 1) return 0;
   return size_t(rows) * heads * p.splits * (c.head_dim + 2) * sizeof(float);
 }
@@ -410,7 +686,7 @@ size_t cache_attention_workspace(const kq_cache& c, const kq_cache_batch& b, boo
 kq_status cache_attention_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q, bool bf16, int64_t rows,
                               int heads, float scale, int window, void* out, int64_t ldo, int32_t* info, void* ws,
                               hipStream_t st) {
-  const Plan p = plan(c, b, heads, window);
+  const Plan p = plan(c, b, bf16, heads, window);
   AttnArgs a;
   a.seq = seq_args(c, b, rows, info);
   a.k = c.k;
@@ -431,8 +707,8 @@ kq_status cache_attention_run(const kq_cache& c, const kq_cache_batch& b, CacheI
   a.splits = p.splits;
   a.part_o = static_cast<float*>(ws);
   a.part_ml = a.part_o + size_t(rows) * heads * p.splits * c.head_dim;
-  if (bf16) return c.head_dim == 64 ? launch<true, 64>(a, st) : launch<true, 128>(a, st);
-  return c.head_dim == 64 ? launch<false, 64>(a, st) : launch<false, 128>(a, st);
+  if (bf16) return c.head_dim == 64 ? launch<true, 64>(a, p.prompt, st) : launch<true, 128>(a, p.prompt, st);
+  return c.head_dim == 64 ? launch<false, 64>(a, p.prompt, st) : launch<false, 128>(a, p.prompt, st);
 }
 
 }  // namespace kq
