@@ -304,7 +304,7 @@ __global__ __launch_bounds__(PAGE * 4) void cache_append_kernel(AppendArgs a) {
         // to bf16 through float32: 2^-8 half a step of bf16, 2^-25 more
         if (BF16)
           *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.q_out) + at) =
-              f32_to_bf16(float(y0)) | (f32_to_bf16(float(y1)) << 16);
+              pack_bf16(float(y0), float(y1));
         else
           *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.q_out) + at) = make_float2(float(y0), float(y1));
       }
@@ -356,8 +356,8 @@ __device__ __forceinline__ void store16(void* out, int64_t at, uint4 codes, floa
     for (int t = 0; t < 4; ++t) f[t] = float(int8_t(w[i] >> (8 * t))) * scale;
     if (BF16) {
       uint2 o;
-      o.x = f32_to_bf16(f[0]) | (f32_to_bf16(f[1]) << 16);
-      o.y = f32_to_bf16(f[2]) | (f32_to_bf16(f[3]) << 16);
+      o.x = pack_bf16(f[0], f[1]);
+      o.y = pack_bf16(f[2], f[3]);
       *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + at + 4 * i) = o;
     } else {
       *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at + 4 * i) = make_float4(f[0], f[1], f[2], f[3]);
@@ -422,7 +422,7 @@ __global__ __launch_bounds__(256) void cache_read_kernel(ReadArgs a) {
       const float f0 = float(int8_t(w0[t >> 2] >> (8 * (t & 3)))) * vs, f1 = float(int8_t(w1[t >> 2] >> (8 * (t & 3)))) * vs;
       const int64_t at = (row0 + t) * a.ld[1] + int64_t(head) * D + 2 * l;
       if (BF16)
-        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out[1]) + at) = f32_to_bf16(f0) | (f32_to_bf16(f1) << 16);
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out[1]) + at) = pack_bf16(f0, f1);
       else
         *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out[1]) + at) = make_float2(f0, f1);
     }

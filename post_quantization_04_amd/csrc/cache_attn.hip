@@ -25,6 +25,7 @@ namespace {
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 constexpr float kNoToken = -1.0e30f;   // running maximum before the first token (finite: no inf - inf)
 constexpr float kZeroScale = -48.0f;   // log2 taken for a value scale of 0: any finite one (its codes are 0)
@@ -85,8 +86,8 @@ template <bool BF16>
 __device__ __forceinline__ void store4(void* p, int64_t at, float a, float b, float c, float d) {
   if (BF16) {
     uint2 u;
-    u.x = f32_to_bf16(a) | (f32_to_bf16(b) << 16);
-    u.y = f32_to_bf16(c) | (f32_to_bf16(d) << 16);
+    u.x = pack_bf16(a, b);
+    u.y = pack_bf16(c, d);
     *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + at) = u;
   } else {
     *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + at) = make_float4(a, b, c, d);
@@ -94,16 +95,22 @@ __device__ __forceinline__ void store4(void* p, int64_t at, float a, float b, fl
 }
 
 // Power of two that takes amax to [2^14, 2^15) (1 for a row of zeros), and its inverse; a row
-// with a NaN or an infinity gets NaN, which reaches all of its scores.
+// with a NaN or an infinity is multiplied by NaN, which reaches all of its scores.
 __device__ __forceinline__ void row_scale(float amax, float& up, float& down) {
   int e;
   (void)frexpf(amax, &e);  // amax = f 2^e, f in [0.5, 1)
   e = amax > 0.0f ? min(max(15 - e, -126), 126) : 0;
   up = amax < INFINITY ? ldexpf(1.0f, e) : NAN;
-  down = amax < INFINITY ? ldexpf(1.0f, -e) : NAN;
+  down = ldexpf(1.0f, -e);
 }
 
 __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Maximum over the lanes l and l + 32, in both.
+__device__ __forceinline__ float across_halves_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 
 // This split's share of the 64-token chunks that a tile of rows sees, and the first and last
 // 16-token groups of the whole tile: what lies outside is never looked up.
@@ -231,7 +238,7 @@ __global__ __launch_bounds__(256, 2) void cache_token_kernel(AttnArgs a) {
       }
     }
     const float f = ks * qf;                                   // scores to base-2 exponents
-    const float lv = vs == 0.0f ? kZeroScale : __log2f(vs);
+    const float lv = vs > 0.0f ? __log2f(vs) : vs == 0.0f ? kZeroScale : NAN;
     const float iv = vs == 0.0f ? 0x1p48f : 1.0f / vs;
     const int t0 = 64 * c + 16 * lk;                           // this lane's first token
     const bool cut = 64 * c + 63 > p_first || (a.window > 0 && 64 * c <= p_last - a.window);
@@ -322,35 +329,55 @@ __global__ __launch_bounds__(256, 2) void cache_token_kernel(AttnArgs a) {
 
 // ---------------------------------------------------------------------------
 // Prompts
+//
+// A workgroup takes 256 rows of one sequence and head, eight waves of 32, and walks the context in tiles of 64
+// tokens. The codes of a tile are loaded and unpacked to float16 once a workgroup, into LDS, three tiles deep:
+// unpacking takes five vector instructions for four codes and is the cost that many rows have to share.
+//
+// What bounds it is the SIMDs' vector issue, not the matrix pipe (measured on an 8192-token prompt over 32 heads):
+// a 32 x 32 x 16 MFMA keeps the matrix pipe busy for 32 cycles and the issue port for about 12 of them, an
+// exponential takes the port for 16, the others for 4. Removing the unpacking alone, or the exponentials alone,
+// saved a sixth of the time each. So the instructions around a score are few: one fused multiply-add (the block's
+// scales and the maximum are its operands), the exponential, an addition and half a conversion; the maximum is
+// taken by threes; the accumulators are rescaled only when the maximum has grown by 2^4; one wave in turn prepares
+// a tile's scales. MFMAs and vector instructions of one wave alternate (half a tile's weights with the other
+// half's scores).
 // ---------------------------------------------------------------------------
 
-// A block's scales as the weights use them. A NaN (a poisoned block, a bad page) becomes a finite
-// stand-in and `bad`: the rows that see such a block are made NaN apart.
+// A block's scales as the weights use them, finite where they multiply scores. A NaN (a poisoned block, a bad
+// page) becomes a weight of 2^100 for whoever sees a token of it, and a NaN in their sum.
 struct BlockScale {
-  float ks, lv, iv, bad;
+  float ks, lv, iv, unused;
 };
 
 __device__ __forceinline__ BlockScale block_scale(float ks, float vs) {
+  const bool bad = !(ks == ks && vs == vs);
   BlockScale r;
-  r.bad = ks == ks && vs == vs ? 0.0f : 1.0f;
-  r.ks = ks > 0.0f ? ks : 1.0f;                 // 0: the codes are 0, so any factor will do
-  r.lv = vs > 0.0f ? __log2f(vs) : kZeroScale;
-  r.iv = vs > 0.0f ? 1.0f / vs : 0x1p48f;
+  r.ks = bad ? 0x1p-100f : ks > 0.0f ? ks : 1.0f;            // 0: the codes are 0, so any factor will do
+  r.lv = bad ? 100.0f : vs > 0.0f ? __log2f(vs) : kZeroScale;
+  r.iv = bad ? NAN : vs > 0.0f ? __builtin_amdgcn_rcpf(vs) : 0x1p48f;   // the reciprocal a unit of float32 off
+  r.unused = 0.0f;
   return r;
 }
 
-template <bool BF16, int D, int NQ, int W>
-__global__ __launch_bounds__(W * 64, NQ == 1 ? 2 : 1) void cache_prompt_kernel(AttnArgs a) {
-  typedef float floatx16 __attribute__((ext_vector_type(16)));
-  constexpr int NT = W * 64, ROWS = 32 * NQ * W;
+template <bool BF16, int D>
+__global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
+  constexpr int NT = 512, ROWS = 256;
   constexpr int KS = D / 16, DT = D / 32;        // MFMA steps over channels, 32-channel output tiles
-  constexpr int KU = D / 8;                      // 16-byte units of a key row in LDS
+  // LDS rows in 16-byte units, of an odd number of them so that lanes reading one unit of consecutive rows meet
+  // different banks, and every step's address is a constant away from the lane's first. Keys: the token of the
+  // product's row r in place r, values: by channel.
+  constexpr int KP = D / 8 + 1, VP = 9;
+  constexpr int KB = 64 * KP, VB = D * VP;       // units of a tile
   constexpr int CH = 8 * D / NT;                 // 16-byte chunks of codes a thread stages (keys, then values)
   constexpr int P = BF16 ? 1 : 2;                // float16 pieces of a query and a weight
-  __shared__ half8 sk[2][64 * KU];               // keys: token rows of KU units
-  __shared__ half8 sv[2][D * 8];                 // values: channel rows of 64 tokens
-  __shared__ BlockScale sc[2][4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // The running maximum of a bf16 row may lag by 2^4, so that accumulators are seldom rescaled; weights, held
+  // times 2^11, then stay below 2^15. A float32 row's never lags.
+  constexpr float kLag = BF16 ? 4.0f : 0.0f, kExp = BF16 ? 11.0f : 14.0f;
+  __shared__ half8 sk[3 * KB];
+  __shared__ half8 sv[3 * VB];
+  __shared__ BlockScale sc[4][4];                // of a tile's four 16-token groups
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 7;
   const int lq = lane & 31, lh = lane >> 5;
   int64_t id = blockIdx.x;
   const int nbh = a.batch * a.kvh;
@@ -364,19 +391,16 @@ __global__ __launch_bounds__(W * 64, NQ == 1 ? 2 : 1) void cache_prompt_kernel(A
   const int first = s.len - s.n;
   const Range rg = chunk_range(s, tile * ROWS / a.g, (min(tile * ROWS + ROWS, nrows) - 1) / a.g, a.window, split, a.splits);
 
-  // this wave's rows
-  const int w0 = tile * ROWS + wave * 32 * NQ;
-  const int wlast = min(w0 + 32 * NQ, nrows) - 1;
-  const int p_hi = wlast >= w0 ? first + wlast / a.g : -1, p_lo = first + min(w0, nrows - 1) / a.g;
-  half8 qf[P][NQ][KS];
-  float fq[NQ];
-  int pos[NQ];
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const int r = min(w0 + 32 * n + lq, nrows - 1);
-    const int i = r / a.g, hd = kh * a.g + (r - i * a.g);
-    pos[n] = first + i;
-    const int64_t at = (int64_t(s.row0) + i) * a.ldq + int64_t(hd) * D + 8 * lh;
+  // this wave's rows, a lane's row and its position
+  const int w0 = tile * ROWS + wave * 32;
+  const int p_hi = w0 < nrows ? first + (min(w0 + 32, nrows) - 1) / a.g : -1, p_lo = first + min(w0, nrows - 1) / a.g;
+  const int r = min(w0 + lq, nrows - 1);
+  const int i = r / a.g, head = kh * a.g + (r - i * a.g);
+  const int pos = first + i;
+  half8 qf[P][KS];
+  float fq;
+  {
+    const int64_t at = (int64_t(s.row0) + i) * a.ldq + int64_t(head) * D + 8 * lh;
     float amax = 0.0f;
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
@@ -396,196 +420,221 @@ __global__ __launch_bounds__(W * 64, NQ == 1 ? 2 : 1) void cache_prompt_kernel(A
       for (int j = 0; j < 8; ++j) {
         const float y = x[j] * up;
         const _Float16 h = _Float16(y);
-        qf[0][n][t][j] = h;
-        if (!BF16) qf[P - 1][n][t][j] = _Float16(y - float(h));
+        qf[0][t][j] = h;
+        if (!BF16) qf[P - 1][t][j] = _Float16(y - float(h));
       }
     }
-    fq[n] = a.scale_log2e * down;
+    fq = a.scale_log2e * down;
   }
 
-  // staging: chunk x < 4 D of keys (token x / (D / 16), 16 channels), then of values (group, channel);
-  // a wave's chunks are all of one 16-token group
+  // Staging: chunk x < 4 D of keys (token x / (D / 16), 16 channels), then of values (group, channel); a wave's
+  // chunks are all of one 16-token group, D chunks of either side. The table's entries are loaded a tile before
+  // the codes and scales that they lead to, those a tile before they are unpacked.
   uint4 raw[CH];
-  float2 rscale;
+  int entry[CH];
+  bool lost = false;                             // an entry of the table that is no page (told at the end)
   const int page = 1 << a.seq.page_log2;
-  auto group_of = [&](int i) {
-    return ((wave * 64 + NT * i) & (4 * D - 1)) / D;       // 16 tokens are D chunks of either side
+  auto group = [&](int c, int x) { return min(max(4 * c + x, rg.g0), rg.g1); };
+  auto of_keys = [&](int n) { return NT * (n + 1) <= 4 * D || (NT * n < 4 * D && wave * 64 + NT * n < 4 * D); };
+  auto chunk_group = [&](int n) { return ((wave * 64 + NT * n) & (4 * D - 1)) / D; };
+  auto look = [&](int c) {
+#pragma unroll
+    for (int n = 0; n < CH; ++n) entry[n] = table_entry(a.seq, b, group(c, chunk_group(n)) << 4);
   };
   auto fetch = [&](int c) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int g = min(max(4 * c + group_of(i), rg.g0), rg.g1);
-      const int pg = max(page_of(a.seq, b, g << 4), 0);
-      const int x = tid + NT * i, y = x & (D - 1);
-      const int64_t at = ((int64_t(pg) * a.kvh + kh) * page + ((g << 4) & (page - 1))) * D + 16 * y;
-      raw[i] = *reinterpret_cast<const uint4*>((wave * 64 + NT * i < 4 * D ? a.k : a.v) + at);
-    }
-    if (tid < 4) {
-      const int g = min(max(4 * c + tid, rg.g0), rg.g1);
-      const int pg = page_of(a.seq, b, g << 4);
-      const int64_t at = int64_t(max(pg, 0)) * a.kvh + kh;
-      rscale = pg < 0 ? make_float2(NAN, NAN) : make_float2(a.k_scale[at], a.v_scale[at]);
+    for (int n = 0; n < CH; ++n) {
+      const int pg = __builtin_amdgcn_readfirstlane(entry[n]);
+      const int64_t at = (int64_t(is_page(a.seq, pg) ? pg : 0) * a.kvh + kh) * (int64_t(page) * D) +
+                         ((group(c, chunk_group(n)) << 4) & (page - 1)) * D;
+      raw[n] = *reinterpret_cast<const uint4*>((of_keys(n) ? a.k : a.v) + at + 16 * ((tid + NT * n) & (D - 1)));
     }
   };
-  auto stage = [&](int buf) {
+  // The scales of a tile are one wave's work, in turn: four groups in its lanes, the same three steps.
+  int entry_s = 0;
+  float2 rscale = make_float2(1.0f, 1.0f);
+  auto look_s = [&](int c) { entry_s = table_entry(a.seq, b, group(c, lane & 3) << 4); };
+  auto fetch_s = [&] {
+    const bool ok = is_page(a.seq, entry_s);
+    const int64_t at = int64_t(ok ? entry_s : 0) * a.kvh + kh;
+    rscale = make_float2(a.k_scale[at], a.v_scale[at]);
+  };
+  auto stage_s = [&](int slot) {
+    const bool ok = is_page(a.seq, entry_s);
+    lost |= !ok;
+    if (lane < 4) sc[slot][lane] = block_scale(ok ? rscale.x : NAN, rscale.y);
+  };
+  // token 16 x + 4 y + z of a 32-token block is row 8 y + 4 x + z of its product: half x of the lanes gets the
+  // scores of tokens 16 x .. 16 x + 15, all of one cache block
+  auto key_row = [](int tok) { return (tok & 35) | ((tok & 12) << 1) | ((tok >> 2) & 4); };
+  int put[CH];                                   // this thread's places in a tile
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int x = tid + NT * i, y = x & (4 * D - 1);
-      const half8 h0 = unpack8(raw[i].x, raw[i].y), h1 = unpack8(raw[i].z, raw[i].w);
-      if (wave * 64 + NT * i < 4 * D) {
-        const int tok = y / (D / 16), u = 2 * (y % (D / 16));
-        const int z = (tok & 3) | ((tok >> 2) & 4);
-        sk[buf][tok * KU + (u ^ z)] = h0;
-        sk[buf][tok * KU + ((u + 1) ^ z)] = h1;
-      } else {
-        const int grp = y / D, d = y % D;
-        sv[buf][d * 8 + ((2 * grp) ^ (d & 7))] = h0;
-        sv[buf][d * 8 + ((2 * grp + 1) ^ (d & 7))] = h1;
-      }
+  for (int n = 0; n < CH; ++n) {
+    const int y = (tid + NT * n) & (4 * D - 1);
+    const int tok = y / (D / 16);
+    put[n] = of_keys(n) ? key_row(tok) * KP + 2 * (y % (D / 16)) : (y % D) * VP + 2 * (y / D);
+  }
+  auto stage = [&](int slot, int n0, int n1) {   // chunks n0 .. n1 - 1
+#pragma unroll
+    for (int n = n0; n < n1; ++n) {
+      const half8 h0 = unpack8(raw[n].x, raw[n].y), h1 = unpack8(raw[n].z, raw[n].w);
+      half8* const to = of_keys(n) ? sk + slot * KB + put[n] : sv + slot * VB + put[n];
+      to[0] = h0;
+      to[1] = h1;
     }
-    if (tid < 4) sc[buf][tid] = block_scale(rscale.x, rscale.y);
   };
 
-  floatx16 o[NQ][DT];
-  float m[NQ], l[NQ];
+  floatx16 o[DT];
+  float m = kNoToken, l = 0.0f;
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    m[n] = kNoToken;
-    l[n] = 0.0f;
+  for (int t = 0; t < DT; ++t) o[t] = floatx16{};
+  const int kat = lq * KP + lh, vat = lq * VP + 2 * lh;
+  // Scores of half h of the tile in a slot: e[x] of this lane belongs to token 64 c + 32 h + 16 lh + x.
+  auto key_step = [&](int slot, int h, int t, floatx16& e) {
+    const half8 kf = (sk + slot * KB + kat)[h * 32 * KP + 2 * t];
+#pragma unroll
+    for (int q = 0; q < P; ++q) e = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[q][t], t + q ? e : floatx16{}, 0, 0, 0);
+  };
+  auto hide = [&](int c, int h, floatx16& e) {                 // scores that the row must not see
+    const int z = 64 * c + 32 * h;
+    if (z + 31 <= p_lo && !(a.window > 0 && z <= p_hi - a.window)) return;
+    const int hi = pos - (z + 16 * lh), lo = a.window > 0 ? hi - a.window : -(1 << 30);
+#pragma unroll
+    for (int x = 0; x < 16; ++x) e[x] = (x <= hi && x > lo) ? e[x] : -INFINITY;
+  };
+  // The running maximum takes the scores of a half in; f is what turns them into exponents.
+  auto raise = [&](const floatx16& e, float f, float lv) {
+    float x0 = e[0], x1 = e[1];
+#pragma unroll
+    for (int x = 2; x < 16; x += 2) {
+      x0 = fmaxf(x0, e[x]);
+      x1 = fmaxf(x1, e[x + 1]);
+    }
+    const float mx = across_halves_max(fmaf(fmaxf(x0, x1), f, lv));
+    if (__any(mx > m + kLag)) {
+      const float mn = fmaxf(m, mx), fall = exp2_raw(m - mn);
+      m = mn;
+      l *= fall;
+#pragma unroll
+      for (int t = 0; t < DT; ++t) o[t] *= fall;
+    }
+  };
+  auto factor = [&](const BlockScale& bs) {
+    return fmaxf(bs.ks * fq, 1e-37f);            // above 0, so that a hidden score stays -inf
+  };
+  // Half h of tile c from its scores e on: the weights alternate with the products of the queries and the next
+  // half's keys (to en), then the products with the values with the unpacking of chunk `part` of a later tile.
+  // A wave's MFMAs and vector instructions overlap only where they alternate.
+  auto half_body = [&](int c, int h, const BlockScale& bs, float f, const floatx16& e, int slot, int kslot, floatx16& en,
+                       auto&& unpack) {
+    const float shift = bs.lv - m + kExp;
+    float sum = 0.0f;
+    half8 pf[P][2];
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      key_step(kslot, h ^ 1, t, en);
+      constexpr int PER = 16 / KS;               // weights between two steps
+#pragma unroll
+      for (int x = t * PER; x < (t + 1) * PER; x += 2) {
+        const float w_0 = exp2_raw(fmaf(e[x], f, shift)), w_1 = exp2_raw(fmaf(e[x + 1], f, shift));
+        const half2v p = {_Float16(w_0), _Float16(w_1)};
+        pf[0][x >> 3][x & 7] = p[0];
+        pf[0][x >> 3][(x & 7) + 1] = p[1];
+        // the sum takes the weights as they were: divided by a small value scale, one that float16 loses can count
+        sum += w_0;
+        sum += w_1;
+        if (!BF16) {
+          pf[P - 1][x >> 3][x & 7] = _Float16(w_0 - float(p[0]));
+          pf[P - 1][x >> 3][(x & 7) + 1] = _Float16(w_1 - float(p[1]));
+        }
+      }
+    }
+    l = sum > 0.0f ? fmaf(sum, bs.iv, l) : l;    // a poisoned block that the row does not see stays out of it
+    unpack();
+    const half8* const vr = sv + slot * VB + vat + 4 * h;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int t = 0; t < DT; ++t) {
+        const half8 vf = vr[32 * VP * t + k];
+#pragma unroll
+        for (int q = 0; q < P; ++q) o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[q][k], o[t], 0, 0, 0);
+      }
+  };
+
+  const int n_tiles = rg.c1 - rg.c0;
+  floatx16 e0, e1;
+  if (n_tiles > 0) {
+    look(rg.c0);
+    fetch(rg.c0);
+    look(rg.c0 + 1);
+    stage(0, 0, CH);
+    fetch(rg.c0 + 1);
+    look(rg.c0 + 2);
+    stage(1, 0, CH);
+    fetch(rg.c0 + 2);
+    look(rg.c0 + 3);
+    if (wave < 4) {                              // scales of tile `wave`; 2 and 3 go on like those of later tiles
+      look_s(rg.c0 + wave);
+      if (wave < 3) fetch_s();
+      if (wave < 2) stage_s(wave);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < KS; ++t) key_step(0, 0, t, e0);
+  }
+  int now = 0, next = 1, far = 2;                // slots of tiles t0, t0 + 1, t0 + 2
+  for (int t0 = 0; t0 < n_tiles; ++t0) {
+    const int c = rg.c0 + t0;
+    const BlockScale b0 = sc[t0 & 3][lh], b1 = sc[t0 & 3][2 + lh];
+    const float f0 = factor(b0), f1 = factor(b1);
+    hide(c, 0, e0);
+    raise(e0, f0, b0.lv);
+    half_body(c, 0, b0, f0, e0, now, now, e1, [&] { stage(far, 0, CH / 2); });
+    hide(c, 1, e1);
+    raise(e1, f1, b1.lv);
+    half_body(c, 1, b1, f1, e1, now, next, e0, [&] {
+      stage(far, CH / 2, CH);
+      fetch(c + 3);
+      look(c + 4);
+    });
+    if (((t0 + 2) & 7) == wave) stage_s((t0 + 2) & 3);
+    if (((t0 + 3) & 7) == wave) fetch_s();
+    if (((t0 + 4) & 7) == wave) look_s(c + 4);
+    __syncthreads();
+    const int was = now;
+    now = next;
+    next = far;
+    far = was;
+  }
+  if (lost) report(a.seq.info, KQ_INFO_PAGE);
+  l += __shfl_xor(l, 32);
+  if (w0 + lq >= nrows) return;
+  const int64_t row = int64_t(s.row0) + i;
+  if (pos < 0) {                                 // sees nothing, whatever its query holds
+    l = 0.0f;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
-      for (int x = 0; x < 16; ++x) o[n][t][x] = 0.0f;
+      for (int x = 0; x < 16; ++x) o[t][x] = 0.0f;
   }
-  // token of this lane's key row in a 32-token block, and its bank swizzle
-  const int ktok = 16 * ((lq >> 2) & 1) + 4 * (lq >> 3) + (lq & 3);
-  const int kz = (ktok & 3) | ((ktok >> 2) & 4);
-
-  if (rg.c0 < rg.c1) {
-    fetch(rg.c0);
-    stage(0);
-    fetch(rg.c0 + 1);
-  }
-  __syncthreads();
-  for (int c = rg.c0; c < rg.c1; ++c) {
-    const int buf = (c - rg.c0) & 1;
-    stage(buf ^ 1);
-    fetch(c + 2);
-    const bool active = 64 * c <= p_hi && (a.window <= 0 || 64 * c + 63 > p_lo - a.window);
-    if (active) {
-      floatx16 e[NQ][2];
+  if (a.splits == 1) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-      for (int n = 0; n < NQ; ++n)
+    for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+      for (int x = 0; x < 4; ++x)
+        store4<BF16>(a.out, row * a.ldo + int64_t(head) * D + 32 * t + 8 * x + 4 * lh, o[t][4 * x] * inv,
+                     o[t][4 * x + 1] * inv, o[t][4 * x + 2] * inv, o[t][4 * x + 3] * inv);
+  } else {
+    const int64_t at = (row * a.heads + head) * a.splits + split;
 #pragma unroll
-          for (int x = 0; x < 16; ++x) e[n][h][x] = 0.0f;
+    for (int t = 0; t < DT; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int t = 0; t < KS; ++t) {
-          const half8 kf = sk[buf][(32 * h + ktok) * KU + ((2 * t + lh) ^ kz)];
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int q = 0; q < P; ++q) e[n][h] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[q][n][t], e[n][h], 0, 0, 0);
-        }
-      const BlockScale b0 = sc[buf][lh], b1 = sc[buf][2 + lh];
-      const bool cut = 64 * c + 63 > p_lo || (a.window > 0 && 64 * c <= p_hi - a.window);
-      half8 pf[P][NQ][4];
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        // tokens x of half h are 64 c + 32 h + 16 lh + x
-        const int hi = pos[n] - (64 * c + 16 * lh), lo = a.window > 0 ? hi - a.window : -(1 << 30);
-        if (cut) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int x = 0; x < 16; ++x) e[n][h][x] = (32 * h + x <= hi && 32 * h + x > lo) ? e[n][h][x] : -INFINITY;
-        }
-        float f0 = b0.ks * fq[n], f1 = b1.ks * fq[n];
-        f0 = f0 < 1e-37f ? 1e-37f : f0;          // above 0, so that a hidden score stays -inf (a NaN stays NaN)
-        f1 = f1 < 1e-37f ? 1e-37f : f1;
-        float x0 = e[n][0][0], x1 = e[n][1][0];
-#pragma unroll
-        for (int x = 1; x < 16; ++x) {
-          x0 = fmaxf(x0, e[n][0][x]);
-          x1 = fmaxf(x1, e[n][1][x]);
-        }
-        float mx = fmaxf(fmaf(x0, f0, b0.lv), fmaf(x1, f1, b1.lv));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        if (__any(mx > m[n])) {
-          const float mn = fmaxf(m[n], mx), fall = exp2_raw(m[n] - mn);
-          m[n] = mn;
-          l[n] *= fall;
-#pragma unroll
-          for (int t = 0; t < DT; ++t) o[n][t] *= fall;
-        }
-        const float s0 = b0.lv - m[n] + kWeightExp, s1 = b1.lv - m[n] + kWeightExp;
-        float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const float w_0 = exp2_raw(fmaf(e[n][0][x], f0, s0)), w_1 = exp2_raw(fmaf(e[n][1][x], f1, s1));
-          sum0 += w_0;
-          sum1 += w_1;
-          const _Float16 h_0 = _Float16(w_0), h_1 = _Float16(w_1);
-          pf[0][n][x >> 3][x & 7] = h_0;
-          pf[0][n][2 + (x >> 3)][x & 7] = h_1;
-          if (!BF16) {
-            pf[P - 1][n][x >> 3][x & 7] = _Float16(w_0 - float(h_0));
-            pf[P - 1][n][2 + (x >> 3)][x & 7] = _Float16(w_1 - float(h_1));
-          }
-        }
-        l[n] += sum0 * b0.iv + sum1 * b1.iv;
-        if (__any((b0.bad != 0.0f) | (b1.bad != 0.0f))) {   // rows that see a poisoned block
-          if ((b0.bad != 0.0f && hi >= 0 && lo < 15) || (b1.bad != 0.0f && hi >= 32 && lo < 47)) l[n] = NAN;
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < DT; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {             // 32-token half k >> 1, its step k & 1
-          const half8 vf = sv[buf][(32 * t + lq) * 8 + ((4 * (k >> 1) + 2 * lh + (k & 1)) ^ (lq & 7))];
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int q = 0; q < P; ++q) o[n][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[q][n][k], o[n][t], 0, 0, 0);
-        }
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const int r = w0 + 32 * n + lq;
-    l[n] += __shfl_xor(l[n], 32);
-    if (r >= nrows) continue;
-    const int i = r / a.g, head = kh * a.g + (r - i * a.g);
-    const int64_t row = int64_t(s.row0) + i;
-    if (pos[n] < 0) {                             // sees nothing, whatever its query holds
-      l[n] = 0.0f;
-#pragma unroll
-      for (int t = 0; t < DT; ++t)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) o[n][t][x] = 0.0f;
-    }
-    if (a.splits == 1) {
-      const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
-#pragma unroll
-      for (int t = 0; t < DT; ++t)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          store4<BF16>(a.out, row * a.ldo + int64_t(head) * D + 32 * t + 8 * x + 4 * lh, o[n][t][4 * x] * inv,
-                       o[n][t][4 * x + 1] * inv, o[n][t][4 * x + 2] * inv, o[n][t][4 * x + 3] * inv);
-    } else {
-      const int64_t at = (row * a.heads + head) * a.splits + split;
-#pragma unroll
-      for (int t = 0; t < DT; ++t)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          *reinterpret_cast<floatx4*>(a.part_o + at * D + 32 * t + 8 * x + 4 * lh) =
-              floatx4{o[n][t][4 * x], o[n][t][4 * x + 1], o[n][t][4 * x + 2], o[n][t][4 * x + 3]};
-      if (lh == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m[n], l[n]);
-    }
+      for (int x = 0; x < 4; ++x)
+        *reinterpret_cast<floatx4*>(a.part_o + at * D + 32 * t + 8 * x + 4 * lh) =
+            floatx4{o[t][4 * x], o[t][4 * x + 1], o[t][4 * x + 2], o[t][4 * x + 3]};
+    if (lh == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m, l);
   }
 }
 
@@ -659,7 +708,7 @@ kq_status launch(const AttnArgs& a, bool prompt, hipStream_t st) {
   kq_status r;
   if (prompt) {
     LaunchTimer timer("cache_prompt_kernel", st);
-    hipLaunchKernelGGL((cache_prompt_kernel<BF16, D, 1, 8>), grid, dim3(512), 0, st, a);
+    hipLaunchKernelGGL((cache_prompt_kernel<BF16, D>), grid, dim3(512), 0, st, a);
     r = check_launch("cache_prompt_kernel");
   } else {
     LaunchTimer timer("cache_token_kernel", st);

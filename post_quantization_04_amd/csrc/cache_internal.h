@@ -55,21 +55,26 @@ __device__ __forceinline__ Seq sequence(const SeqArgs& a, int b, bool tell) {
   return s;
 }
 
+// Entry of the table for position p of sequence b, and whether it is a page.
+__device__ __forceinline__ int table_entry(const SeqArgs& a, int b, int p) {
+  return a.table[int64_t(b) * a.max_pages + (p >> a.page_log2)];
+}
+
+__device__ __forceinline__ bool is_page(const SeqArgs& a, int id) { return uint32_t(id) < uint64_t(a.pages); }
+
 // Page of position p of sequence b; -1 (and told) when the table's entry is not a page.
 __device__ __forceinline__ int page_of(const SeqArgs& a, int b, int p) {
-  const int id = a.table[int64_t(b) * a.max_pages + (p >> a.page_log2)];
-  if (uint32_t(id) < uint64_t(a.pages)) return id;
+  const int id = table_entry(a, b, p);
+  if (is_page(a, id)) return id;
   report(a.info, KQ_INFO_PAGE);
   return -1;
 }
 
-__device__ __forceinline__ float bf16_to_f32(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
-
-// Round to nearest even; NaN stays NaN.
-__device__ __forceinline__ uint32_t f32_to_bf16(float x) {
-  const uint32_t u = __float_as_uint(x);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return (u >> 16) | 0x40u;
-  return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+// Two floats to bf16, the first in the low half (to nearest even; NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float floatx2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2{a, b}), bf16x2));
 }
 
 }  // namespace kq
