@@ -20,6 +20,7 @@
 namespace kq {
 namespace {
 
+constexpr int kHeadsPerWave = 8;                       // of a long prompt's queries, all loads in flight
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100: keeps 1 / scale and its sums finite
 
 struct AppendArgs {
@@ -62,42 +63,81 @@ __device__ __forceinline__ double row_sum(double v) {
   return v;
 }
 
-// Norm and rotation of a row's entries e = 2 l and 2 l + 1 in the lanes of that row. w: the
-// norm's weights of the two (with `norm`), cs: this position's row of the table.
+// What a lane needs of one position's row of the rotations for its entries 2 l and 2 l + 1: y <- y c + p s with
+// the partner p of each (in `from`'s lane for pairs half a rotation apart, the lane's other entry when
+// interleaved), on the lanes below rot_dim.
+struct Turn {
+  float2 c, s;
+  bool in;
+};
+
 template <int D>
-__device__ __forceinline__ void place(double& y0, double& y1, bool norm, float2 w, double eps, const float* cs, int rot,
-                                      bool interleaved, int l) {
-  constexpr int LPR = D / 2;
-  if (norm) {
-    const double r = 1.0 / sqrt(row_sum<LPR>(y0 * y0 + y1 * y1) * (1.0 / D) + eps);
-    y0 *= r * double(w.x);
-    y1 *= r * double(w.y);
+__device__ __forceinline__ Turn turn_of(const float* row, int rot, bool interleaved, int l) {
+  const int half = rot >> 1;
+  Turn t;
+  t.c = t.s = make_float2(0.0f, 0.0f);
+  t.in = row && 2 * l < rot;
+  if (!row) return t;
+  const bool in = t.in, low = 2 * l < half;
+  if (interleaved) {
+    const float c = row[in ? l : 0], s = row[half + (in ? l : 0)];
+    t.c = make_float2(c, c);
+    t.s = make_float2(-s, s);
+  } else {
+    const int j = in ? (low ? 2 * l : 2 * l - half) : 0;                 // even, as half is
+    const float2 c = *reinterpret_cast<const float2*>(row + j), s = *reinterpret_cast<const float2*>(row + half + j);
+    t.c = c;
+    t.s = low ? make_float2(-s.x, -s.y) : s;
   }
-  if (cs) {
-    const int half = rot >> 1;
+  return t;
+}
+
+// The lane that holds the partners of entries 2 l and 2 l + 1 (every lane of the wave asks).
+__device__ __forceinline__ int partner_lane(int rot, bool interleaved, int l) {
+  const int lane = threadIdx.x & 63;
+  if (interleaved || 2 * l >= rot) return lane;
+  return 4 * l < rot ? lane + (rot >> 2) : lane - (rot >> 2);
+}
+
+// Norm (weights w of the lane's entries, wp of their partners) and rotation of a row's entries x.
+template <int D>
+__device__ __forceinline__ void place(double (&y)[2], float2 x, bool norm, float2 w, float2 wp, double eps, bool turns,
+                                      const Turn& t, int from, bool interleaved) {
+  constexpr int LPR = D / 2;
+  y[0] = x.x;
+  y[1] = x.y;
+  double r = 1.0;
+  if (norm) {
+    r = 1.0 / sqrt(row_sum<LPR>(y[0] * y[0] + y[1] * y[1]) * (1.0 / D) + eps);
+    y[0] *= r * double(w.x);
+    y[1] *= r * double(w.y);
+  }
+  if (turns) {
+    double p0, p1;
     if (interleaved) {
-      if (2 * l < rot) {
-        const double c = cs[l], s = cs[half + l];
-        const double a = y0;
-        y0 = a * c - y1 * s;
-        y1 = y1 * c + a * s;
-      }
+      p0 = y[1];
+      p1 = y[0];
     } else {
-      // entry e < half pairs with e + half, held rot / 4 lanes on (every lane takes part in the exchange)
-      const int lane = threadIdx.x & 63;
-      const bool low = 2 * l < half, in = 2 * l < rot;
-      const int from = in ? (low ? lane + (rot >> 2) : lane - (rot >> 2)) : lane;
-      const double p0 = __shfl(y0, from), p1 = __shfl(y1, from);
-      if (in) {
-        const int j = low ? 2 * l : 2 * l - half;
-        const double c0 = cs[j], c1 = cs[j + 1];
-        const double s0 = low ? -double(cs[half + j]) : double(cs[half + j]);
-        const double s1 = low ? -double(cs[half + j + 1]) : double(cs[half + j + 1]);
-        y0 = y0 * c0 + p0 * s0;
-        y1 = y1 * c1 + p1 * s1;
+      p0 = __shfl(x.x, from);
+      p1 = __shfl(x.y, from);
+      if (norm) {
+        p0 *= r * double(wp.x);
+        p1 *= r * double(wp.y);
       }
     }
+    p0 = y[0] * double(t.c.x) + p0 * double(t.s.x);
+    p1 = y[1] * double(t.c.y) + p1 * double(t.s.y);
+    y[0] = t.in ? p0 : y[0];
+    y[1] = t.in ? p1 : y[1];
   }
+}
+
+// A norm's weights of the lane's entries and of their partners.
+__device__ __forceinline__ void norm_weights(const float* w, int l, int from, float2& own, float2& partner) {
+  own = partner = make_float2(1.0f, 1.0f);
+  if (!w) return;
+  own = *reinterpret_cast<const float2*>(w + 2 * l);
+  partner = make_float2(__shfl(own.x, from), __shfl(own.y, from));
 }
 
 // round_half_even(y / s) in [-127, 127], inv = 1 / s: the product is within 1e-13 of the quotient,
@@ -122,7 +162,9 @@ __device__ void append_block(const AppendArgs& a, bool is_v, int head, int pagei
   const bool turn = !is_v && a.rope != nullptr;
   const void* src = is_v ? a.src[2] : a.src[1];
   const int64_t ld = is_v ? a.ld[2] : a.ld[1];
-  const float2 wt = norm ? *reinterpret_cast<const float2*>(a.norm[1] + 2 * l) : make_float2(1.0f, 1.0f);
+  const int from = turn ? partner_lane(a.rot, a.interleaved, l) : lane;
+  float2 wt, wp;
+  norm_weights(norm ? a.norm[1] : nullptr, l, from, wt, wp);
   float* const scale_at = (is_v ? a.v_scale : a.k_scale) + int64_t(pageid) * a.kvh + head;
   const float s_old = lo > 0 ? *scale_at : 0.0f;
 
@@ -131,20 +173,19 @@ __device__ void append_block(const AppendArgs& a, bool is_v, int head, int pagei
   double amax = 0.0;
   if (mine) {
     float2 x[NS];
+    Turn tn[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const int slot = NS == 1 ? lo : min(max(first_slot + s, lo), hi - 1);
+      const int64_t p = int64_t(pos0) + slot;
       x[s] = load2<BF16>(src, int64_t(row_lo + slot - lo) * ld + int64_t(head) * D + 2 * l);
+      tn[s] = turn_of<D>(turn ? a.rope + (p >= a.rope_len ? 0 : p) * a.rot : nullptr, a.rot, a.interleaved, l);
     }
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const int slot = NS == 1 ? lo : first_slot + s;
-      const int64_t p = pos0 + min(max(slot, lo), hi - 1);
-      y[s][0] = x[s].x;
-      y[s][1] = x[s].y;
-      const bool off = turn && p >= a.rope_len;
-      place<D>(y[s][0], y[s][1], norm, wt, a.eps, turn ? a.rope + (off ? 0 : p) * a.rot : nullptr, a.rot,
-               a.interleaved, l);
+      const bool off = turn && int64_t(pos0) + slot >= a.rope_len;
+      place<D>(y[s], x[s], norm, wt, wp, a.eps, turn, tn[s], from, a.interleaved);
       if (slot >= lo && slot < hi) {
         if (off) {
           report(a.seq.info, KQ_INFO_POSITION);
@@ -278,37 +319,40 @@ __global__ __launch_bounds__(PAGE * 4) void cache_append_kernel(AppendArgs a) {
   const Seq s = sequence(a.seq, b, false);
   if (i >= s.n) return;
   const int64_t p = int64_t(s.len) - s.n + i;
-  const bool norm = a.norm[0] != nullptr;
-  const float2 wt = norm ? *reinterpret_cast<const float2*>(a.norm[0] + 2 * l) : make_float2(1.0f, 1.0f);
-  const bool off = p < 0 || (a.rope && p >= a.rope_len);
-  if (off && a.rope && p >= a.rope_len && lane == 0) report(a.seq.info, KQ_INFO_POSITION);
-  const float* cs = a.rope ? a.rope + (off ? 0 : p) * a.rot : nullptr;
+  const bool norm = a.norm[0] != nullptr, turn = a.rope != nullptr;
+  const int from = turn ? partner_lane(a.rot, a.interleaved, l) : lane;
+  float2 wt, wp;
+  norm_weights(a.norm[0], l, from, wt, wp);
+  const bool off = p < 0 || (turn && p >= a.rope_len);
+  if (turn && p >= a.rope_len && lane == 0) report(a.seq.info, KQ_INFO_POSITION);
+  const Turn tn = turn_of<D>(turn ? a.rope + (off ? 0 : p) * a.rot : nullptr, a.rot, a.interleaved, l);
   const int64_t row = s.row0 + i;
   const int h_per = (a.heads + a.q_groups - 1) / a.q_groups;
   const int h1 = min(a.heads, (gq + 1) * h_per);
-  constexpr int RW = 64 / LPR;  // heads a wave takes at a time
-  for (int h0 = gq * h_per; h0 < h1; h0 += 4 * RW) {
-    float2 x[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      x[u] = load2<BF16>(a.src[0], row * a.ld[0] + int64_t(min(h0 + u * RW + hh, h1 - 1)) * D + 2 * l);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (h0 + u * RW >= h1) break;  // uniform
-      double y0 = x[u].x, y1 = x[u].y;
-      place<D>(y0, y1, norm, wt, a.eps, cs, a.rot, a.interleaved, l);
-      if (off) y0 = y1 = NAN;
-      const int h = h0 + u * RW + hh;
-      if (h < h1) {
-        const int64_t at = row * a.ldqo + int64_t(h) * D + 2 * l;
-        // to bf16 through float32: 2^-8 half a step of bf16, 2^-25 more
-        if (BF16)
-          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.q_out) + at) =
-              pack_bf16(float(y0), float(y1));
-        else
-          *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.q_out) + at) = make_float2(float(y0), float(y1));
-      }
+  constexpr int RW = 64 / LPR, UN = kHeadsPerWave / RW;   // heads a wave takes at once, and how often
+  const int h0 = gq * h_per;
+  auto finish = [&](int h, float2 x) {
+    double y[2];
+    place<D>(y, x, norm, wt, wp, a.eps, turn, tn, from, a.interleaved);
+    if (off) y[0] = y[1] = NAN;
+    if (h < h1) {
+      const int64_t at = row * a.ldqo + int64_t(h) * D + 2 * l;
+      // to bf16 through float32: half a step of bf16 (2^-8), and 2^-25
+      if (BF16)
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.q_out) + at) = pack_bf16(float(y[0]), float(y[1]));
+      else
+        *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.q_out) + at) = make_float2(float(y[0]), float(y[1]));
     }
+  };
+  auto source = [&](int h) { return load2<BF16>(a.src[0], row * a.ld[0] + int64_t(min(h, h1 - 1)) * D + 2 * l); };
+  if (h_per <= RW) {
+    finish(h0 + hh, source(h0 + hh));
+  } else {
+    float2 x[UN];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) x[u] = source(h0 + u * RW + hh);
+#pragma unroll
+    for (int u = 0; u < UN; ++u) finish(h0 + u * RW + hh, x[u]);
   }
 }
 
@@ -464,7 +508,7 @@ kq_status cache_append_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q
   a.kv_wgs = int64_t(b.batch) * a.blocks * c.kv_heads * 2;
   const int waves = c.page / 16;
   // a wave takes 8 heads of a token; all heads of a few tokens are spread wider, for latency
-  const int per_wave = int64_t(b.batch) * b.max_q * heads > 8192 ? 8 : (c.head_dim == 64 ? 2 : 1);
+  const int per_wave = int64_t(b.batch) * b.max_q * heads > 8192 ? kHeadsPerWave : 128 / c.head_dim;
   a.q_groups = heads ? (heads + per_wave - 1) / per_wave : 1;
   const int64_t per_b = (int64_t(b.max_q) * a.q_groups + waves - 1) / waves * waves;
   const int64_t q_wgs = q_out ? int64_t(b.batch) * per_b / waves : 0;

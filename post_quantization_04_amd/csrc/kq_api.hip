@@ -430,8 +430,8 @@ kq_status kq_cache_append(const kq_cache* cache, const kq_cache_batch* batch, co
   if ((st = cache_tensor(what, "v", v, dtype, rows, cache->kv_heads, cache->head_dim, ldv)) != KQ_OK) return st;
   if ((q_norm || k_norm) && !(eps > 0.0f && std::isfinite(eps)))
     return fail(KQ_EINVAL, "%s: eps must be finite and > 0", what);
-  if (((reinterpret_cast<uintptr_t>(q_norm) | reinterpret_cast<uintptr_t>(k_norm)) & 7))
-    return fail(KQ_EINVAL, "%s: norm weights must be 8-byte aligned", what);
+  if ((reinterpret_cast<uintptr_t>(q_norm) | reinterpret_cast<uintptr_t>(k_norm) | reinterpret_cast<uintptr_t>(rope)) & 7)
+    return fail(KQ_EINVAL, "%s: norm weights and rotations must be 8-byte aligned", what);
   if (rope && (rope_len < 1 || rot_dim < 4 || rot_dim % 4 || rot_dim > cache->head_dim))
     return fail(KQ_EINVAL, "%s: rot_dim must be a multiple of 4 up to head_dim, with rope_len >= 1 (rot_dim %d, rope_len %lld)",
                 what, rot_dim, (long long)rope_len);
