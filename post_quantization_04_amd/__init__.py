@@ -521,17 +521,20 @@ _CACHE_DTYPES = None
 
 
 def _cache_tensor(name: str, t, heads: int, cache: KVCache, rows: Optional[int] = None, dtype=None):
-    """(rows, row pitch) of a [rows, heads, head_dim] tensor of a cache call."""
+    """(rows, row pitch) of a [rows, heads, head_dim] tensor of a cache call. Called for every tensor of calls that
+    take microseconds: the message is put together only for a tensor that is refused."""
     shape = t.shape
+    if len(shape) == 3 and t.device == cache.device and (dtype is None or t.dtype == dtype):
+        n, h, d = shape
+        s0, s1, s2 = t.stride()
+        if (d == cache.head_dim and (h == heads or heads == 0) and (rows is None or n == rows) and s2 == 1
+                and (s1 == d or h == 1 or n == 0)):
+            return n, (s0 if n > 1 else h * d)
     _need(len(shape) == 3 and shape[2] == cache.head_dim and (heads == 0 or shape[1] == heads)
           and (rows is None or shape[0] == rows), f"{name}: must be [rows, heads, head_dim]")
     _need(dtype is None or t.dtype == dtype, f"{name}: dtype differs")
     _need(t.device == cache.device, f"{name}: on another device than the cache")
-    stride = t.stride()
-    n, wide = shape[0], shape[1] * shape[2]
-    _need(stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1 or n == 0),
-          f"{name}: a row's heads must be contiguous")
-    return n, (stride[0] if n > 1 else wide)
+    raise KQError(KQ_EINVAL, f"{name}: a row's heads must be contiguous")
 
 
 def _cache_dtype(name: str, t) -> int:
@@ -540,32 +543,36 @@ def _cache_dtype(name: str, t) -> int:
         import torch
         _CACHE_DTYPES = {torch.bfloat16: KQ_BF16, torch.float32: KQ_F32}
     d = _CACHE_DTYPES.get(t.dtype)
-    _need(d is not None, f"{name}: bfloat16 or float32")
+    if d is None:
+        raise KQError(KQ_EINVAL, f"{name}: bfloat16 or float32")
     return d
 
 
 def _cache_info(name: str, info, cache: KVCache):
-    if info is not None:
-        import torch
-        _need(info.dtype == torch.int32 and info.numel() >= 1 and info.device == cache.device,
-              f"{name}: info must be an int32 tensor on the cache's device")
-    return _ptr(info)
+    if info is None:
+        return None
+    import torch
+    _need(info.dtype == torch.int32 and info.numel() >= 1 and info.device == cache.device,
+          f"{name}: info must be an int32 tensor on the cache's device")
+    return info.data_ptr()
 
 
 def _cache_call(name: str, fn, cache: KVCache, batch: CacheBatch, args, stream) -> None:
     """fn(cache, batch, *args, stream) on the cache's device, whichever device is current."""
     import torch
     device = cache.device
-    _need(device.type == "cuda" and batch.device == device, f"{name}: cache and batch must be on one GPU")
+    if device.type != "cuda" or batch.device != device:
+        raise KQError(KQ_EINVAL, f"{name}: cache and batch must be on one GPU")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        raw = torch._C._cuda_getCurrentRawStream(device.index)  # current_stream(device).cuda_stream without the object
     else:
         _need(stream.device == device, f"{name}: the stream belongs to another device")
+        raw = stream.cuda_stream
     if torch.cuda.current_device() == device.index:
-        status = fn(cache.ref, batch.ref, *args, stream.cuda_stream)
+        status = fn(cache.ref, batch.ref, *args, raw)
     else:
         with torch.cuda.device(device):
-            status = fn(cache.ref, batch.ref, *args, stream.cuda_stream)
+            status = fn(cache.ref, batch.ref, *args, raw)
     if status != KQ_OK:
         _check(status, name)
 
@@ -582,19 +589,20 @@ def cache_append(cache: KVCache, batch: CacheBatch, q, k, v, q_out=None, *, q_no
     rows, ldk = _cache_tensor("cache_append: k", k, cache.kv_heads, cache)
     _, ldv = _cache_tensor("cache_append: v", v, cache.kv_heads, cache, rows, k.dtype)
     heads = ldq = ldqo = 0
-    _need((q is None) == (q_out is None), "cache_append: q and q_out come together")
+    if (q is None) != (q_out is None):
+        raise KQError(KQ_EINVAL, "cache_append: q and q_out come together")
     if q is not None:
         heads = q.shape[1]
         _, ldq = _cache_tensor("cache_append: q", q, heads, cache, rows, k.dtype)
         _, ldqo = _cache_tensor("cache_append: q_out", q_out, heads, cache, rows, k.dtype)
     for w in (q_norm, k_norm):
-        if w is not None:
-            _need(w.dtype == torch.float32 and w.shape == (cache.head_dim,) and w.stride(0) == 1
-                  and w.device == cache.device, "cache_append: norm weights are float32 [head_dim] on the cache's device")
+        if w is not None and not (w.dtype == torch.float32 and w.shape == (cache.head_dim,) and w.stride(0) == 1
+                                  and w.device == cache.device):
+            raise KQError(KQ_EINVAL, "cache_append: norm weights are float32 [head_dim] on the cache's device")
     rope_len = rot = 0
     if rope is not None:
-        _need(rope.dim() == 2 and rope.dtype == torch.float32 and rope.is_contiguous() and rope.device == cache.device,
-              "cache_append: rope is contiguous float32 [positions, rot_dim] on the cache's device")
+        if not (rope.dim() == 2 and rope.dtype == torch.float32 and rope.is_contiguous() and rope.device == cache.device):
+            raise KQError(KQ_EINVAL, "cache_append: rope is contiguous float32 [positions, rot_dim] on the cache's device")
         rope_len, rot = rope.shape
     _cache_call(name, lib().kq_cache_append, cache, batch,
                 (_ptr(q), k.data_ptr(), v.data_ptr(), dtype, rows, heads, ldq, ldk, ldv, _ptr(q_norm), _ptr(k_norm), eps,
@@ -639,12 +647,13 @@ def cache_attention(cache: KVCache, batch: CacheBatch, q, out, *, scale: Optiona
     rows, ldq = _cache_tensor("cache_attention: q", q, heads, cache)
     _, ldo = _cache_tensor("cache_attention: out", out, heads, cache, rows, q.dtype)
     if ws is None:
-        ws = cache_attention_workspace(cache, batch, q, window)
-        if stream is not None:
-            ws.record_stream(stream)
-    else:
-        _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == cache.device,
-              "cache_attention: ws is contiguous uint8 on the cache's device")
+        if stream is None:
+            ws = cache_attention_workspace(cache, batch, q, window)
+        else:  # memory of the stream that uses it
+            with torch.cuda.stream(stream):
+                ws = cache_attention_workspace(cache, batch, q, window)
+    elif not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == cache.device):
+        raise KQError(KQ_EINVAL, "cache_attention: ws is contiguous uint8 on the cache's device")
     _cache_call(name, lib().kq_cache_attention, cache, batch,
                 (q.data_ptr(), dtype, rows, heads, ldq, cache.head_dim ** -0.5 if scale is None else scale, window,
-                 out.data_ptr(), ldo, _cache_info(name, info, cache), ws.data_ptr(), ws.numel(), ), stream)
+                 out.data_ptr(), ldo, _cache_info(name, info, cache), ws.data_ptr(), ws.numel()), stream)
