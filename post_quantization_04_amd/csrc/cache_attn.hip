@@ -16,6 +16,7 @@
 // output), for float32 outputs to two pieces. Maxima, sums and accumulators are float32.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "cache_internal.h"
 
@@ -205,23 +206,39 @@ __global__ __launch_bounds__(256, 2) void cache_token_kernel(AttnArgs a) {
   float m = kNoToken, l = 0.0f;
   const int page = 1 << a.seq.page_log2, pmask = page - 1;
 
-  for (int c = rg.c0 + wave; c < rg.c1; c += 4) {
+  // Codes are loaded into the registers of the chunk before as soon as its products have used them, their pages
+  // looked up a chunk earlier still.
+  int idk = 0, idv = 0, offk = 0, offv = 0;
+  uint4 kc[4][U], vc[DT];
+  float ks = 0.0f, vs = 0.0f;
+  bool lost = false;
+  auto look = [&](int c) {
     // 16-token groups of this lane: of its key rows, and of its weights and values
     const int gk = min(max(4 * c + (li >> 2), rg.g0), rg.g1), gv = min(max(4 * c + lk, rg.g0), rg.g1);
-    const int idk = page_of(a.seq, b, gk << 4), idv = page_of(a.seq, b, gv << 4);
-    const int8_t* const kp = a.k + ((int64_t(max(idk, 0)) * a.kvh + kh) * page + ((gk << 4) & pmask)) * D +
-                             (li & 3) * D + 16 * lk;
-    const int64_t blk = int64_t(max(idv, 0)) * a.kvh + kh;
-    const int8_t* const vp = a.v + (blk * page + ((gv << 4) & pmask)) * D + 16 * li;
-    uint4 kc[4][U], vc[DT];
+    idk = table_entry(a.seq, b, gk << 4);
+    idv = table_entry(a.seq, b, gv << 4);
+    offk = (gk << 4) & pmask;
+    offv = (gv << 4) & pmask;
+  };
+  auto load_keys = [&] {
+    const int64_t blk = int64_t(is_page(a.seq, idk) ? idk : 0) * a.kvh + kh;
+    const int8_t* const kp = a.k + (blk * page + offk) * D + (li & 3) * D + 16 * lk;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int u = 0; u < U; ++u) kc[t][u] = *reinterpret_cast<const uint4*>(kp + 4 * t * D + 64 * u);
-    const float ks = idv < 0 ? NAN : a.k_scale[blk], vs = idv < 0 ? NAN : a.v_scale[blk];
+  };
+  auto load_values = [&] {
+    const int64_t blk = int64_t(is_page(a.seq, idv) ? idv : 0) * a.kvh + kh;
+    const int8_t* const vp = a.v + (blk * page + offv) * D + 16 * li;
+    ks = a.k_scale[blk];
+    vs = a.v_scale[blk];
 #pragma unroll
     for (int t = 0; t < DT; ++t) vc[t] = *reinterpret_cast<const uint4*>(vp + 256 * t);
-
+  };
+  bool known = true;                             // whether this lane's block is a page, for the chunk in registers
+  // one chunk; every load is unconditional, so that the waits count those that are still out
+  auto chunk = [&](int c, auto more) {
     floatx4 e[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -237,9 +254,12 @@ __global__ __launch_bounds__(256, 2) void cache_token_kernel(AttnArgs a) {
         }
       }
     }
-    const float f = ks * qf;                                   // scores to base-2 exponents
-    const float lv = vs > 0.0f ? __log2f(vs) : vs == 0.0f ? kZeroScale : NAN;
-    const float iv = vs == 0.0f ? 0x1p48f : 1.0f / vs;
+    if constexpr (more) load_keys();
+    lost |= !known;
+    const float kscale = known ? ks : NAN, vscale = known ? vs : NAN;
+    const float f = kscale * qf;                               // scores to base-2 exponents
+    const float lv = vscale > 0.0f ? __log2f(vscale) : vscale == 0.0f ? kZeroScale : NAN;
+    const float iv = vscale == 0.0f ? 0x1p48f : __builtin_amdgcn_rcpf(vscale);   // a unit of float32 off
     const int t0 = 64 * c + 16 * lk;                           // this lane's first token
     const bool cut = 64 * c + 63 > p_first || (a.window > 0 && 64 * c <= p_last - a.window);
     const int hi = p - t0, lo = a.window > 0 ? hi - a.window : -1;  // tokens x in (lo, hi] are seen
@@ -286,7 +306,23 @@ __global__ __launch_bounds__(256, 2) void cache_token_kernel(AttnArgs a) {
         o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pl[1], o[t], 0, 0, 0);
       }
     }
+    if constexpr (more) {
+      load_values();
+      known = is_page(a.seq, idv);
+      look(c + 8);
+    }
+  };
+  int c = rg.c0 + wave;
+  if (c < rg.c1) {
+    look(c);
+    load_keys();
+    load_values();
+    known = is_page(a.seq, idv);
+    look(c + 4);
+    for (; c + 4 < rg.c1; c += 4) chunk(c, std::true_type{});
+    chunk(c, std::false_type{});
   }
+  if (lost) report(a.seq.info, KQ_INFO_PAGE);
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
 #pragma unroll
