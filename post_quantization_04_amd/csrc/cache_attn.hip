@@ -28,6 +28,7 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
+constexpr int kTokenWaves = 8;          // waves that share a workgroup's range of the context
 constexpr float kNoToken = -1.0e30f;   // running maximum before the first token (finite: no inf - inf)
 constexpr float kZeroScale = -48.0f;   // log2 taken for a value scale of 0: any finite one (its codes are 0)
 constexpr float kWeightExp = 14.0f;    // weights are held times 2^14, so that float16 keeps small ones
@@ -124,7 +125,7 @@ __device__ __forceinline__ Range chunk_range(const Seq& s, int i_first, int i_la
   if (p_last < 0) return Range{0, 0, 0, 0};
   const int low = window > 0 ? max(0, p_first - window + 1) : 0;
   const int a = low >> 6, e = (p_last >> 6) + 1;
-  const int per = max((e - a + splits - 1) / splits, 4);  // at least one chunk for each wave
+  const int per = max((e - a + splits - 1) / splits, kTokenWaves);  // at least one chunk for each wave
   const int c0 = min(a + split * per, e);
   return Range{c0, min(c0 + per, e), low >> 4, p_last >> 4};
 }
@@ -132,7 +133,7 @@ __device__ __forceinline__ Range chunk_range(const Seq& s, int i_first, int i_la
 // ---------------------------------------------------------------------------
 // A few rows a sequence: single tokens, drafts
 //
-// A workgroup takes 16 rows of one sequence and head and a range of the context; its four waves
+// A workgroup takes 16 rows of one sequence and head and a range of the context; its waves
 // take the range's 64-token chunks in turn and never share data before the end, where their
 // partial sums are joined in LDS. Nothing is staged: each operand comes from the cache in the
 // order its MFMA wants it. S^T = K Q^T has tokens as rows: lane (lk = lane / 16, li = lane mod 16)
@@ -143,12 +144,13 @@ __device__ __forceinline__ Range chunk_range(const Seq& s, int i_first, int i_la
 // bytes a lane.
 // ---------------------------------------------------------------------------
 template <bool BF16, int D>
-__global__ __launch_bounds__(256, 2) void cache_token_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnArgs a) {
+  constexpr int W = kTokenWaves;
   constexpr int U = D / 64;       // 16-byte key loads a lane and token row
   constexpr int DT = D / 16;      // 16-channel tiles of the output
   constexpr int PITCH = D + 4;
-  __shared__ float sh_o[4][16 * PITCH];
-  __shared__ float sh_m[4][16], sh_l[4][16];
+  __shared__ float sh_o[W][16 * PITCH];
+  __shared__ float sh_m[W][16], sh_l[W][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int li = lane & 15, lk = lane >> 4;
   int64_t id = blockIdx.x;
@@ -309,7 +311,7 @@ __global__ __launch_bounds__(256, 2) void cache_token_kernel(AttnArgs a) {
     if constexpr (more) {
       load_values();
       known = is_page(a.seq, idv);
-      look(c + 8);
+      look(c + 2 * W);
     }
   };
   int c = rg.c0 + wave;
@@ -318,8 +320,8 @@ __global__ __launch_bounds__(256, 2) void cache_token_kernel(AttnArgs a) {
     load_keys();
     load_values();
     known = is_page(a.seq, idv);
-    look(c + 4);
-    for (; c + 4 < rg.c1; c += 4) chunk(c, std::true_type{});
+    look(c + W);
+    for (; c + W < rg.c1; c += W) chunk(c, std::true_type{});
     chunk(c, std::false_type{});
   }
   if (lost) report(a.seq.info, KQ_INFO_PAGE);
@@ -332,35 +334,31 @@ __global__ __launch_bounds__(256, 2) void cache_token_kernel(AttnArgs a) {
     sh_l[wave][li] = l;
   }
   __syncthreads();
-  // join the waves: 16 threads a row
-  const int q = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * 4;
-  if (tile * 16 + q >= nrows) return;
+  // join the waves: D / 4 threads a row
+  const int q = threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
+  if (q >= 16 || tile * 16 + q >= nrows) return;
   float mj = sh_m[0][q];
 #pragma unroll
-  for (int w = 1; w < 4; ++w) mj = fmaxf(mj, sh_m[w][q]);
-  float fw[4], lj = 0.0f;
+  for (int w = 1; w < W; ++w) mj = fmaxf(mj, sh_m[w][q]);
+  floatx4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+  float lj = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    fw[w] = exp2_raw(sh_m[w][q] - mj);
-    lj += fw[w] * sh_l[w][q];
+  for (int w = 0; w < W; ++w) {
+    const float fw = exp2_raw(sh_m[w][q] - mj);
+    lj += fw * sh_l[w][q];
+    x += fw * *reinterpret_cast<const floatx4*>(&sh_o[w][q * PITCH + d]);
   }
   const int rq = tile * 16 + q, iq = rq / a.g;
   const int64_t row = int64_t(s.row0) + iq;
   const int head = kh * a.g + (rq - iq * a.g);
-#pragma unroll
-  for (int d = d0; d < D; d += 64) {
-    floatx4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) x += fw[w] * *reinterpret_cast<const floatx4*>(&sh_o[w][q * PITCH + d]);
-    if (a.splits == 1) {
-      const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
-      store4<BF16>(a.out, row * a.ldo + int64_t(head) * D + d, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    } else {
-      *reinterpret_cast<floatx4*>(a.part_o + ((row * a.heads + head) * a.splits + split) * D + d) = x;
-    }
+  if (a.splits == 1) {
+    const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
+    store4<BF16>(a.out, row * a.ldo + int64_t(head) * D + d, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+  } else {
+    const int64_t at = (row * a.heads + head) * a.splits + split;
+    *reinterpret_cast<floatx4*>(a.part_o + at * D + d) = x;
+    if (d == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(mj, lj);
   }
-  if (a.splits > 1 && d0 == 0)
-    *reinterpret_cast<float2*>(a.part_ml + ((row * a.heads + head) * a.splits + split) * 2) = make_float2(mj, lj);
 }
 
 // ---------------------------------------------------------------------------
@@ -697,10 +695,12 @@ __global__ __launch_bounds__(256) void cache_join_kernel(AttnArgs a) {
   for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
   floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
   float l = 0.0f;
+#pragma unroll 4
   for (int x = grp; x < a.splits; x += G) {
-    const float f = exp2_raw(ml[2 * x] - m);
+    const float2 w = *reinterpret_cast<const float2*>(ml + 2 * x);
+    const float f = exp2_raw(w.x - m);
     acc += f * *reinterpret_cast<const floatx4*>(po + int64_t(x) * D + d);
-    l += f * ml[2 * x + 1];
+    l += f * w.y;
   }
   sh[grp][threadIdx.x % T] = acc;
   if (threadIdx.x % T == 0) sh_l[grp] = l;
@@ -729,7 +729,7 @@ Plan plan(const kq_cache& c, const kq_cache_batch& b, bool bf16, int heads, int 
   int64_t longest = int64_t(b.max_pages) * c.page;
   if (window > 0) longest = std::min<int64_t>(longest, int64_t(window) + b.max_q + 63);
   const int64_t wgs = int64_t(b.batch) * c.kv_heads * p.tiles;
-  const int64_t want = ((p.prompt ? 1 : 4) * kCus + wgs - 1) / wgs;
+  const int64_t want = (kCus + wgs - 1) / wgs;
   p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, (longest + 511) / 512)));
   return p;
 }
@@ -748,7 +748,7 @@ kq_status launch(const AttnArgs& a, bool prompt, hipStream_t st) {
     r = check_launch("cache_prompt_kernel");
   } else {
     LaunchTimer timer("cache_token_kernel", st);
-    hipLaunchKernelGGL((cache_token_kernel<BF16, D>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((cache_token_kernel<BF16, D>), grid, dim3(kTokenWaves * 64), 0, st, a);
     r = check_launch("cache_token_kernel");
   }
   if (r != KQ_OK || a.splits == 1) return r;
