@@ -387,17 +387,25 @@ def attention_case(seed, dtype, heads, kvh, dim, page, lens, news, *, window=0, 
     q = _bf16(q) if dtype == "bf16" else q.astype(np.float32)
     scale = dim ** -0.5 if scale is None else scale
     qd = _dev(np.concatenate((q, q[:, :1]), 1), dtype)[:, :heads]      # a pitch of its own
-    out = torch.full((rows, heads + 1, dim), 9.0, dtype=qd.dtype, device=DEV)[:, :heads]
-    info = torch.zeros(1, dtype=torch.int32, device=DEV)
-    dev, b = upload(cache), batch_of(table, lens, q_start, max_q)
-    w = kq.cache_attention_workspace(dev, b, qd) if ws else None
-    if w is not None and w.numel():
-        w.fill_(255)                                                   # NaN wherever it is read before it is written
-    kq.cache_attention(dev, b, qd, out, scale=scale, window=window, info=info, ws=w)
-    got = out.float().cpu().numpy()
-    assert (got[int(q_start[-1]):] == 9.0).all()
-    check_attention(got, cache, table, lens, q_start, q, scale, window, dtype)
-    return got, int(info.item())
+    dev = upload(cache)
+    told = set()
+    # the kernel goes by the bound on the rows of a sequence: as given, with the first one that takes the prompts' kernel
+    # (few workgroups, so a long context is split there too), and with one that fills the GPU
+    first = max(max(news), -(-max(16 * (256 // (len(lens) * kvh) + 1), 65) // (heads // kvh)))
+    for bound in (max_q, first, 8192):
+        out = torch.full((rows, heads + 1, dim), 9.0, dtype=qd.dtype, device=DEV)[:, :heads]
+        info = torch.zeros(1, dtype=torch.int32, device=DEV)
+        b = batch_of(table, lens, q_start, bound)
+        w = kq.cache_attention_workspace(dev, b, qd) if ws else None
+        if w is not None and w.numel():
+            w.fill_(255)                                               # NaN wherever it is read before it is written
+        kq.cache_attention(dev, b, qd, out, scale=scale, window=window, info=info, ws=w)
+        got = out.float().cpu().numpy()
+        assert (got[int(q_start[-1]):] == 9.0).all()
+        check_attention(got, cache, table, lens, q_start, q, scale, window, dtype)
+        told.add(int(info.item()))
+    assert len(told) == 1
+    return got, told.pop()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -543,17 +551,18 @@ def test_attention_wrong_entries_are_told():
         return host(out), int(info.item())
 
     table = [[0, 1, 2, 3], [4, 5, 6, 7]]
-    good, info = run(table, [64, 40], [0, 10, 20])
-    assert info == 0
-    for lens in ([64, -1], [64, 65], [2 ** 31 - 1, 40]):
-        out, info = run(table, lens, [0, 10, 20])
-        assert info == kq.KQ_INFO_LENGTH
-        if lens[1] == -1:
-            assert not out[10:].any()
-        np.testing.assert_array_equal(out[:10], good[:10])  # 2^31 - 1 counts as the table's 64
-    for q_start in ([0, 10, 21], [-1, 10, 20], [0, 12, 10]):
-        _, info = run(table, [64, 40], q_start)
-        assert info == kq.KQ_INFO_ROWS
+    for bound in (20, 9000):                     # the single tokens' kernel and the prompts'
+        good, info = run(table, [64, 40], [0, 10, 20], bound)
+        assert info == 0
+        for lens in ([64, -1], [64, 65], [2 ** 31 - 1, 40]):
+            out, info = run(table, lens, [0, 10, 20], bound)
+            assert info == kq.KQ_INFO_LENGTH
+            if lens[1] == -1:
+                assert not out[10:].any()
+            np.testing.assert_array_equal(out[:10], good[:10])  # 2^31 - 1 counts as the table's 64
+        for q_start in ([0, 10, 21], [-1, 10, 20], [0, 12, 10]):
+            _, info = run(table, [64, 40], q_start, bound)
+            assert info == kq.KQ_INFO_ROWS
     out, info = run(table, [64, 40], [0, 10, 20], max_q=4)
     assert info == kq.KQ_INFO_ROWS
 
@@ -571,10 +580,10 @@ def test_attention_offsets_past_32_bits():
     at = torch.tensor(far, device=DEV)
     for name in ("k", "v", "k_scale", "v_scale"):
         getattr(dev, name)[at] = to_dev(getattr(small, name))
-    for new in (1, 40):
+    for new, bound in ((1, None), (40, None), (40, 8192)):
         q = rng.standard_normal((new, 16, dim)).astype(np.float32)
         out = torch.empty((new, 16, dim), device=DEV)
-        kq.cache_attention(dev, batch_of([far], [600], [0, new]), to_dev(q), out)
+        kq.cache_attention(dev, batch_of([far], [600], [0, new], bound), to_dev(q), out)
         check_attention(host(out), small, [[0, 1, 2, 3, 4]], [600], [0, new], q, dim ** -0.5, 0, "f32")
     k, v = torch.empty((600, kvh, dim), device=DEV), torch.empty((600, kvh, dim), device=DEV)
     kq.cache_read(dev, batch_of([far], [600], [0, 600]), k, v)
@@ -598,7 +607,7 @@ def test_calls_repeat_bit_for_bit_and_on_other_streams():
     rng = np.random.default_rng(17)
     table, pages = tables(rng, [4000, 900], 32)
     dev = upload(filled(rng, pages, 32, 2, 128))
-    for news in ([1, 1], [200, 40]):
+    for news in ([1, 1], [200, 40], [3000, 600]):
         q = to_dev(rng.standard_normal((sum(news), 8, 128)).astype(np.float32))
         b = batch_of(table, [4000, 900], np.concatenate(([0], np.cumsum(news))))
         first = torch.empty_like(q)
