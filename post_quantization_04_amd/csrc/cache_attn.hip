@@ -46,7 +46,7 @@ struct AttnArgs {
   int heads, kvh, g;
   float scale_log2e;
   int window;
-  int batch, tiles, splits;
+  int batch, tiles, tile_rows, splits;
   float* part_o;    // [rows * heads][splits][D], sum of weights (times 2^14) times codes
   float* part_ml;   // [rows * heads][splits][2]: m, sum of weights (times 2^14) / s_v
 };
@@ -114,20 +114,21 @@ __device__ __forceinline__ float across_halves_max(float x) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// This split's share of the 64-token chunks that a tile of rows sees, and the first and last
-// 16-token groups of the whole tile: what lies outside is never looked up.
+// This split's share [c0, c1) of the 64-token chunks that a tile of rows sees, the first and last 16-token
+// groups of the whole tile (what lies outside is never looked up), and in how many parts the tile is split: a
+// tile of one part is written by its workgroup, the others' parts are joined.
 struct Range {
-  int c0, c1, g0, g1;
+  int c0, c1, g0, g1, parts;
 };
 
-__device__ __forceinline__ Range chunk_range(const Seq& s, int i_first, int i_last, int window, int split, int splits) {
+__device__ __forceinline__ Range chunk_range(const AttnArgs& a, const Seq& s, int i_first, int i_last, int split) {
   const int p_last = s.len - s.n + i_last, p_first = s.len - s.n + i_first;
-  if (p_last < 0) return Range{0, 0, 0, 0};
-  const int low = window > 0 ? max(0, p_first - window + 1) : 0;
-  const int a = low >> 6, e = (p_last >> 6) + 1;
-  const int per = max((e - a + splits - 1) / splits, kTokenWaves);  // at least one chunk for each wave
-  const int c0 = min(a + split * per, e);
-  return Range{c0, min(c0 + per, e), low >> 4, p_last >> 4};
+  if (p_last < 0) return Range{0, 0, 0, 0, 1};
+  const int low = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
+  const int c = low >> 6, n = (p_last >> 6) + 1 - c;
+  const int per = max((n + a.splits - 1) / a.splits, 8);   // single tokens: a chunk for each wave
+  const int c0 = min(c + split * per, c + n);
+  return Range{c0, min(c0 + per, c + n), low >> 4, p_last >> 4, (n + per - 1) / per};
 }
 
 // ---------------------------------------------------------------------------
@@ -167,7 +168,8 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
   const int i = r / a.g, hd = kh * a.g + (r - i * a.g);
   const int p = first + i;                         // its position
   const int i_first = tile * 16 / a.g, i_last = (min(tile * 16 + 16, nrows) - 1) / a.g;
-  const Range rg = chunk_range(s, i_first, i_last, a.window, split, a.splits);
+  const Range rg = chunk_range(a, s, i_first, i_last, split);
+  if (split >= rg.parts) return;
   // every token of a chunk is seen by every row if it lies in (p_last - window, p_first]
   const int p_first = first + i_first, p_last = first + i_last;
 
@@ -351,7 +353,7 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
   const int rq = tile * 16 + q, iq = rq / a.g;
   const int64_t row = int64_t(s.row0) + iq;
   const int head = kh * a.g + (rq - iq * a.g);
-  if (a.splits == 1) {
+  if (rg.parts == 1) {
     const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
     store4<BF16>(a.out, row * a.ldo + int64_t(head) * D + d, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
   } else {
@@ -423,7 +425,8 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
   const int nrows = s.n * a.g;
   if (tile * ROWS >= nrows) return;
   const int first = s.len - s.n;
-  const Range rg = chunk_range(s, tile * ROWS / a.g, (min(tile * ROWS + ROWS, nrows) - 1) / a.g, a.window, split, a.splits);
+  const Range rg = chunk_range(a, s, tile * ROWS / a.g, (min(tile * ROWS + ROWS, nrows) - 1) / a.g, split);
+  if (split >= rg.parts) return;
 
   // this wave's rows, a lane's row and its position
   const int w0 = tile * ROWS + wave * 32;
@@ -659,7 +662,7 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
 #pragma unroll
       for (int x = 0; x < 16; ++x) o[t][x] = 0.0f;
   }
-  if (a.splits == 1) {
+  if (rg.parts == 1) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -679,79 +682,103 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
   }
 }
 
-// Joins the splits of each row: a workgroup for each (sequence, token, head), 256 threads as
-// 256 * 4 / D groups of D / 4 threads that take the splits in turn, a fixed order.
-template <bool BF16, int D>
+// Joins the parts of each row: D / 4 threads for four channels each, and G such groups that take the parts in
+// turn, in a fixed order; 256 * 4 / (D G) rows a workgroup. G 1 for many rows or a few parts, else all groups
+// of a workgroup for one row.
+template <bool BF16, int D, int G>
 __global__ __launch_bounds__(256) void cache_join_kernel(AttnArgs a) {
-  constexpr int T = D / 4, G = 256 / T;
+  constexpr int T = D / 4, R = 256 / (T * G);
   __shared__ floatx4 sh[G][T];
   __shared__ float sh_l[G];
-  int64_t id = blockIdx.x;
-  const int head = id % a.heads;
-  id /= a.heads;
-  const int i = id % a.seq.max_q, b = id / a.seq.max_q;
+  const int grp = threadIdx.x / T % G, d = threadIdx.x % T * 4;
+  const int per_b = a.seq.max_q * a.heads;       // below 2^31: checked by the host
+  const int wgs_b = (per_b + R - 1) / R;
+  const int b = blockIdx.x / wgs_b, in = (blockIdx.x - b * wgs_b) * R + threadIdx.x / (T * G);
+  const int i = in / a.heads, head = in - i * a.heads;
   const Seq s = sequence(a.seq, b, false);
-  if (i >= s.n) return;
+  if (i >= s.n) return;                          // with G > 1 for the whole workgroup
+  const int row_tile = (i * a.g + head % a.g) / a.tile_rows * a.tile_rows, nrows = s.n * a.g;
+  const int parts = chunk_range(a, s, row_tile / a.g, (min(row_tile + a.tile_rows, nrows) - 1) / a.g, 0).parts;
+  if (parts == 1) return;
   const int64_t row = int64_t(s.row0) + i;
   const float* const ml = a.part_ml + (row * a.heads + head) * a.splits * 2;
   const float* const po = a.part_o + (row * a.heads + head) * a.splits * int64_t(D);
-  const int lane = threadIdx.x & 63, grp = threadIdx.x / T, d = (threadIdx.x % T) * 4;
   float m = kNoToken;
-  for (int x = lane; x < a.splits; x += 64) m = fmaxf(m, ml[2 * x]);
+  if (G > 1) {
+    const int lane = threadIdx.x & 63;
+    for (int x = lane; x < parts; x += 64) m = fmaxf(m, ml[2 * x]);
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+    for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+  } else {
+    for (int x = 0; x < parts; ++x) m = fmaxf(m, ml[2 * x]);
+  }
   floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
   float l = 0.0f;
 #pragma unroll 4
-  for (int x = grp; x < a.splits; x += G) {
+  for (int x = grp; x < parts; x += G) {
     const float2 w = *reinterpret_cast<const float2*>(ml + 2 * x);
     const float f = exp2_raw(w.x - m);
     acc += f * *reinterpret_cast<const floatx4*>(po + int64_t(x) * D + d);
     l += f * w.y;
   }
-  sh[grp][threadIdx.x % T] = acc;
-  if (threadIdx.x % T == 0) sh_l[grp] = l;
-  __syncthreads();
-  if (grp) return;
+  if (G > 1) {
+    sh[grp][d / 4] = acc;
+    if (d == 0) sh_l[grp] = l;
+    __syncthreads();
+    if (grp) return;
 #pragma unroll
-  for (int x = 1; x < G; ++x) {
-    acc += sh[x][threadIdx.x];
-    l += sh_l[x];
+    for (int x = 1; x < G; ++x) {
+      acc += sh[x][d / 4];
+      l += sh_l[x];
+    }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   store4<BF16>(a.out, row * a.ldo + int64_t(head) * D + d, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
 }
 
+template <bool BF16, int D, int G>
+kq_status launch_join(const AttnArgs& a, hipStream_t st) {
+  constexpr int R = 1024 / (D * G);
+  const int64_t wgs = a.batch * ((int64_t(a.seq.max_q) * a.heads + R - 1) / R);
+  {
+    LaunchTimer timer("cache_join_kernel", st);
+    hipLaunchKernelGGL((cache_join_kernel<BF16, D, G>), dim3(static_cast<uint32_t>(wgs)), dim3(256), 0, st, a);
+  }
+  return check_launch("cache_join_kernel");
+}
+
 struct Plan {
   bool prompt;
-  int tiles, splits;
+  int tile_rows, tiles, splits;
 };
 
-Plan plan(const kq_cache& c, const kq_cache_batch& b, bool bf16, int heads, int window) {
+Plan plan(const kq_cache& c, const kq_cache_batch& b, int heads, int window) {
   Plan p;
   const int64_t rows = int64_t(b.max_q) * (heads / c.kv_heads), heads_all = int64_t(b.batch) * c.kv_heads;
   // 16 rows a workgroup while those fill the GPU once at most, or while 256 rows would be mostly idle: one
   // sequence, 8 key/value heads, 4096 tokens: 256 rows 24.6 us against 34.5 in tiles of 256, 384 rows about even;
   // 8 sequences: 64 rows 31.6 against 46.9, 128 rows 57.9 against 54.5
   p.prompt = rows > 64 && heads_all * ((rows + 15) / 16) > kCus;
-  const int rows_wg = p.prompt ? 256 : 16;
-  p.tiles = static_cast<int>((rows + rows_wg - 1) / rows_wg);
+  p.tile_rows = p.prompt ? 256 : 16;
+  p.tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
   int64_t longest = int64_t(b.max_pages) * c.page;
   if (window > 0) longest = std::min<int64_t>(longest, int64_t(window) + b.max_q + 63);
-  // the context is split while that leaves one workgroup a CU at most (two rounds of half the work cost as much as
-  // one), and a split has enough tokens to pay for the joining launch (single tokens, 32 over 8 heads: 1024 tokens
-  // 11.4 us in two of 512, 11.8 whole; 64 channels: 9.3 and 7.6)
-  const int64_t most = std::max<int64_t>(1, kCus / (heads_all * p.tiles));
-  const int64_t least = p.prompt ? 512 : 65536 / c.head_dim;
+  // The context is split while that leaves one workgroup a CU at most, and a split has enough tokens to pay for the
+  // joining launch (single tokens, 32 over 8 heads: 1024 tokens 11.4 us in two of 512, 11.8 whole; 64 channels: 9.3
+  // and 7.6). More workgroups than that are never split, not even where the last tiles of a prompt outlast the
+  // others: 2048 tokens, 32 over 8 heads, 256 workgroups of 1 to 32 chunks in parts of 17 took 87 us and 16 more to
+  // join, whole 77 (workgroups start in order, in rotation over the shader engines, so long and short ones in turn
+  // end up on the same CUs).
+  const int64_t most = std::max<int64_t>(1, kCus / (heads_all * p.tiles)), least = p.prompt ? 512 : 65536 / c.head_dim;
   p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (longest + least - 1) / least)));
+  if (window > 0) p.splits = std::min(p.splits, plan(c, b, heads, 0).splits);   // fits in the workspace of window 0
   return p;
 }
 
 template <bool BF16, int D>
 kq_status launch(const AttnArgs& a, bool prompt, hipStream_t st) {
   const int64_t wgs = int64_t(a.batch) * a.kvh * a.tiles * a.splits;
-  const int64_t joins = int64_t(a.batch) * a.seq.max_q * a.heads;
-  if (wgs > int64_t(INT32_MAX) || (a.splits > 1 && joins > int64_t(INT32_MAX)))
+  if (wgs > int64_t(INT32_MAX) || (a.splits > 1 && int64_t(a.seq.max_q) * a.heads * a.batch > int64_t(INT32_MAX)))
     return fail(KQ_EUNSUPPORTED, "kq_cache_attention: too many workgroups (batch %d, max_q %d)", a.batch, a.seq.max_q);
   const dim3 grid(static_cast<uint32_t>(wgs));
   kq_status r;
@@ -765,18 +792,16 @@ kq_status launch(const AttnArgs& a, bool prompt, hipStream_t st) {
     r = check_launch("cache_token_kernel");
   }
   if (r != KQ_OK || a.splits == 1) return r;
-  {
-    LaunchTimer timer("cache_join_kernel", st);
-    hipLaunchKernelGGL((cache_join_kernel<BF16, D>), dim3(static_cast<uint32_t>(joins)), dim3(256), 0, st, a);
-  }
-  return check_launch("cache_join_kernel");
+  // 32 heads of 4 tokens, 8 parts: 13.2 us a call against 13.5 with one group a row; of 256 tokens 52.7 and 45.4
+  const bool few_rows = int64_t(a.batch) * a.seq.max_q * a.heads <= 1024;
+  return a.splits > 4 && few_rows ? launch_join<BF16, D, 1024 / D>(a, st) : launch_join<BF16, D, 1>(a, st);
 }
 
 }  // namespace
 
 size_t cache_attention_workspace(const kq_cache& c, const kq_cache_batch& b, bool bf16, int64_t rows, int heads,
                                  int window) {
-  const Plan p = plan(c, b, bf16, heads, window);
+  const Plan p = plan(c, b, heads, window);
   if (p.splits == 1) return 0;
   return size_t(rows) * heads * p.splits * (c.head_dim + 2) * sizeof(float);
 }
@@ -784,7 +809,7 @@ size_t cache_attention_workspace(const kq_cache& c, const kq_cache_batch& b, boo
 kq_status cache_attention_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q, bool bf16, int64_t rows,
                               int heads, float scale, int window, void* out, int64_t ldo, int32_t* info, void* ws,
                               hipStream_t st) {
-  const Plan p = plan(c, b, bf16, heads, window);
+  const Plan p = plan(c, b, heads, window);
   AttnArgs a;
   a.seq = seq_args(c, b, rows, info);
   a.k = c.k;
@@ -802,6 +827,7 @@ kq_status cache_attention_run(const kq_cache& c, const kq_cache_batch& b, CacheI
   a.window = window;
   a.batch = b.batch;
   a.tiles = p.tiles;
+  a.tile_rows = p.tile_rows;
   a.splits = p.splits;
   a.part_o = static_cast<float*>(ws);
   a.part_ml = a.part_o + size_t(rows) * heads * p.splits * c.head_dim;
