@@ -7,13 +7,13 @@
 // head_dim 128, two rows of 32 lanes at 64). Each value is read once and each code written once;
 // the layout of the values (16 tokens of a channel side by side) makes a lane's 16 slots one
 // 16-byte store for each of its channels. Queries need no scale and go to workgroups of their
-// own in the same launch, a wave for each token and group of heads.
+// own, a wave for each token and group of heads.
 //
-// Arithmetic is float64 from the loaded value to the code: with float32 a norm, a rotation and
-// a division end within 1e-5 of a step of a rounding border for one entry in 10^5, whose code
-// then depends on the order of operations. A float64 operation issues at float32's rate on
-// gfx950.
+// Norm and rotation are float64, and so is the division where float32 cannot tell the code: in
+// float32 alone they end within 1e-5 of a step of a rounding border for one entry in 10^5, whose
+// code would then depend on the order of operations.
 #include <cmath>
+#include <type_traits>
 
 #include "cache_internal.h"
 
@@ -140,20 +140,37 @@ __device__ __forceinline__ void norm_weights(const float* w, int l, int from, fl
   partner = make_float2(__shfl(own.x, from), __shfl(own.y, from));
 }
 
-// round_half_even(y / s) in [-127, 127], inv = 1 / s: the product is within 1e-13 of the quotient,
-// so only a value that close to a border needs the division itself.
-__device__ __forceinline__ int code_of(double y, double s, double inv) {
-  const double t = y * inv;
-  double r = rint(t);
-  if (fabs(fabs(t - r) - 0.5) < 1e-12) r = rint(y / s);
-  return int(fmin(fmax(r, -127.0), 127.0));
+// round_half_even(y / s) in [-127, 127]. The float32 product with inv = 1 / s is within 3 roundings of the
+// quotient, 127 * 3 * 2^-24 = 2.3e-5: only a value that close to a border needs the float64 division (a wave has
+// one in the slots of a block at times, so the whole wave takes it).
+template <typename T>
+__device__ __forceinline__ void codes_of(const T (&y)[2], double s, float inv, int (&c)[2]) {
+  float r[2];
+  bool near = false;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float t = float(y[e]) * inv;
+    r[e] = rintf(t);
+    near |= fabsf(fabsf(t - r[e]) - 0.5f) < 4e-5f;
+  }
+  if (__any(near)) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) r[e] = float(rint(double(y[e]) / s));
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) c[e] = int(__builtin_amdgcn_fmed3f(r[e], -127.0f, 127.0f));
 }
+
+__device__ __forceinline__ float max_abs(float a, float y) { return fmaxf(a, fabsf(y)); }
+__device__ __forceinline__ double max_abs(double a, double y) { return fmax(a, fabs(y)); }
 
 __device__ __forceinline__ int rescaled(int code, double ratio) { return int(rint(double(code) * ratio)); }
 
-// One block of one side. NS 1: the block takes one new token (slot lo), which every lane computes.
-template <bool BF16, int D, int PAGE, int NS>
-__device__ void append_block(const AppendArgs& a, bool is_v, int head, int pageid, int pos0, int lo, int hi, int row_lo) {
+// One block of one side: values are float32 as they come, keys float64 from the norm and the rotation on. NS 1:
+// the block takes one new token (slot lo), which every lane computes.
+template <bool BF16, int D, int PAGE, int NS, bool is_v>
+__device__ void append_block(const AppendArgs& a, int head, int pageid, int pos0, int lo, int hi, int row_lo) {
+  using T = typename std::conditional<is_v, float, double>::type;
   constexpr int LPR = D / 2, SL = 16 * LPR / 64;  // lanes a row, slots a lane
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int l = lane & (LPR - 1), hh = lane / LPR;
@@ -168,35 +185,51 @@ __device__ void append_block(const AppendArgs& a, bool is_v, int head, int pagei
   float* const scale_at = (is_v ? a.v_scale : a.k_scale) + int64_t(pageid) * a.kvh + head;
   const float s_old = lo > 0 ? *scale_at : 0.0f;
 
-  double y[NS][2];
+  T y[NS][2];
   const bool mine = NS == 1 || (16 * w < hi && 16 * w + 16 > lo);  // uniform in the wave
-  double amax = 0.0;
+  T top = 0, poison = 0;  // poison: NaN once an entry is not finite (0 * inf)
   if (mine) {
     float2 x[NS];
-    Turn tn[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const int slot = NS == 1 ? lo : min(max(first_slot + s, lo), hi - 1);
-      const int64_t p = int64_t(pos0) + slot;
       x[s] = load2<BF16>(src, int64_t(row_lo + slot - lo) * ld + int64_t(head) * D + 2 * l);
-      tn[s] = turn_of<D>(turn ? a.rope + (p >= a.rope_len ? 0 : p) * a.rot : nullptr, a.rot, a.interleaved, l);
+    }
+    if constexpr (is_v) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        y[s][0] = x[s].x;
+        y[s][1] = x[s].y;
+      }
+    } else {
+      constexpr int STEP = NS < 4 ? NS : 4;      // slots whose rotations are loaded together
+#pragma unroll
+      for (int s0 = 0; s0 < NS; s0 += STEP) {
+        Turn tn[STEP];
+#pragma unroll
+        for (int s = 0; s < STEP; ++s) {
+          const int slot = NS == 1 ? lo : min(max(first_slot + s0 + s, lo), hi - 1);
+          const int64_t p = int64_t(pos0) + slot;
+          tn[s] = turn_of<D>(turn ? a.rope + (p >= a.rope_len ? 0 : p) * a.rot : nullptr, a.rot, a.interleaved, l);
+        }
+#pragma unroll
+        for (int s = 0; s < STEP; ++s)
+          place<D>(y[s0 + s], x[s0 + s], norm, wt, wp, a.eps, turn, tn[s], from, a.interleaved);
+      }
     }
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const int slot = NS == 1 ? lo : first_slot + s;
-      const bool off = turn && int64_t(pos0) + slot >= a.rope_len;
-      place<D>(y[s], x[s], norm, wt, wp, a.eps, turn, tn[s], from, a.interleaved);
-      if (slot >= lo && slot < hi) {
-        if (off) {
-          report(a.seq.info, KQ_INFO_POSITION);
-          y[s][0] = NAN;
-        }
-        // infinite for a NaN too, which a plain maximum would drop
-        amax = fmax(amax, fabs(y[s][0]) < INFINITY ? fabs(y[s][0]) : INFINITY);
-        amax = fmax(amax, fabs(y[s][1]) < INFINITY ? fabs(y[s][1]) : INFINITY);
+      if (turn && slot >= lo && slot < hi && int64_t(pos0) + slot >= a.rope_len) {
+        report(a.seq.info, KQ_INFO_POSITION);
+        poison = NAN;
       }
+      // slots that are not new hold a copy of one that is
+      top = max_abs(max_abs(top, y[s][0]), y[s][1]);
+      poison = fma(y[s][0], T(0), fma(y[s][1], T(0), poison));
     }
   }
+  double amax = poison == poison ? double(top) : double(INFINITY);
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) amax = fmax(amax, __shfl_xor(amax, o));
   if (PAGE > 16) {
@@ -210,7 +243,8 @@ __device__ void append_block(const AppendArgs& a, bool is_v, int head, int pagei
   if (!(s_new >= s_old)) s_new = s_old;                       // a NaN of the block stays
   if (!(amax < INFINITY) || !(s_new < INFINITY)) s_new = NAN;
   if (threadIdx.x == 0) *scale_at = s_new;
-  const double sd = s_new, inv = s_new > 0.0f ? 1.0 / sd : 0.0;
+  const double sd = s_new;
+  const float inv = s_new > 0.0f ? 1.0f / s_new : 0.0f;
   const bool usable = s_new > 0.0f;                           // not 0, not NaN
   const bool grow = lo > 0 && s_old > 0.0f && s_new > s_old;
   const double ratio = grow ? double(s_old) / sd : 1.0;
@@ -221,9 +255,10 @@ __device__ void append_block(const AppendArgs& a, bool is_v, int head, int pagei
   int c[NS][2];
   if (mine) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) c[s][e] = usable ? code_of(y[s][e], sd, inv) : 0;
+    for (int s = 0; s < NS; ++s) {
+      if (usable) codes_of(y[s], sd, inv, c[s]);
+      else c[s][0] = c[s][1] = 0;
+    }
   }
   const int64_t block = int64_t(pageid) * a.kvh + head;
   if (!is_v) {
@@ -280,36 +315,12 @@ __device__ void append_block(const AppendArgs& a, bool is_v, int head, int pagei
   }
 }
 
-template <bool BF16, int D, int PAGE>
-__global__ __launch_bounds__(PAGE * 4) void cache_append_kernel(AppendArgs a) {
-  constexpr int LPR = D / 2, SL = 16 * LPR / 64, WAVES = PAGE / 16;
-  int64_t id = blockIdx.x;
-  if (id < a.kv_wgs) {
-    const int side = id & 1;
-    id >>= 1;
-    const int head = id % a.kvh;
-    id /= a.kvh;
-    const int j = id % a.blocks, b = id / a.blocks;
-    const Seq s = sequence(a.seq, b, j == 0 && head == 0 && side == 0 && threadIdx.x == 0);
-    if (s.n <= 0) return;
-    const int first = s.len - s.n;  // position of the first new token; below 0: those tokens have no place
-    if (first < 0 && j == 0 && threadIdx.x == 0) report(a.seq.info, KQ_INFO_LENGTH);
-    if ((int64_t(max(first, 0) / PAGE) + j) * PAGE >= s.len) return;
-    const int pos0 = (max(first, 0) / PAGE + j) * PAGE;
-    const int lo = max(max(first, 0) - pos0, 0), hi = min(PAGE, s.len - pos0);
-    const int pageid = page_of(a.seq, b, pos0);
-    if (pageid < 0) return;
-    const int row_lo = s.row0 + pos0 + lo - first;
-    if (hi - lo == 1)
-      append_block<BF16, D, PAGE, 1>(a, side, head, pageid, pos0, lo, hi, row_lo);
-    else
-      append_block<BF16, D, PAGE, SL>(a, side, head, pageid, pos0, lo, hi, row_lo);
-    return;
-  }
-  // queries: a wave for each token and group of heads
-  id -= a.kv_wgs;
+// Queries: a wave for each token and group of heads.
+template <bool BF16, int D, int WAVES>
+__device__ void turn_queries(const AppendArgs& a, int64_t wg) {
+  constexpr int LPR = D / 2;
   const int lane = threadIdx.x & 63, l = lane & (LPR - 1), hh = lane / LPR;
-  const int64_t item = id * WAVES + (threadIdx.x >> 6);
+  const int64_t item = wg * WAVES + (threadIdx.x >> 6);
   const int64_t items = int64_t(a.seq.max_q) * a.q_groups;
   const int64_t per_b = (items + WAVES - 1) / WAVES * WAVES;
   const int b = item / per_b;
@@ -354,6 +365,44 @@ __global__ __launch_bounds__(PAGE * 4) void cache_append_kernel(AppendArgs a) {
 #pragma unroll
     for (int u = 0; u < UN; ++u) finish(h0 + u * RW + hh, x[u]);
   }
+}
+
+template <bool BF16, int D, int PAGE>
+__global__ __launch_bounds__(PAGE * 4) void cache_append_kernel(AppendArgs a) {
+  constexpr int SL = D / 8, WAVES = PAGE / 16;
+  int64_t id = blockIdx.x;
+  if (id < a.kv_wgs) {
+    const int side = id & 1;
+    id >>= 1;
+    const int head = id % a.kvh;
+    id /= a.kvh;
+    const int j = id % a.blocks, b = id / a.blocks;
+    const Seq s = sequence(a.seq, b, j == 0 && head == 0 && side == 0 && threadIdx.x == 0);
+    if (s.n <= 0) return;
+    const int first = s.len - s.n;  // position of the first new token; below 0: those tokens have no place
+    if (first < 0 && j == 0 && threadIdx.x == 0) report(a.seq.info, KQ_INFO_LENGTH);
+    if ((int64_t(max(first, 0) / PAGE) + j) * PAGE >= s.len) return;
+    const int pos0 = (max(first, 0) / PAGE + j) * PAGE;
+    const int lo = max(max(first, 0) - pos0, 0), hi = min(PAGE, s.len - pos0);
+    const int pageid = page_of(a.seq, b, pos0);
+    if (pageid < 0) return;
+    const int row_lo = s.row0 + pos0 + lo - first;
+    if (hi - lo == 1) {
+      if (side) append_block<BF16, D, PAGE, 1, true>(a, head, pageid, pos0, lo, hi, row_lo);
+      else append_block<BF16, D, PAGE, 1, false>(a, head, pageid, pos0, lo, hi, row_lo);
+    } else {
+      if (side) append_block<BF16, D, PAGE, SL, true>(a, head, pageid, pos0, lo, hi, row_lo);
+      else append_block<BF16, D, PAGE, SL, false>(a, head, pageid, pos0, lo, hi, row_lo);
+    }
+    return;
+  }
+  turn_queries<BF16, D, WAVES>(a, id - a.kv_wgs);
+}
+
+// The queries of many tokens, on their own: the blocks' kernel needs twice the registers.
+template <bool BF16, int D>
+__global__ __launch_bounds__(256) void cache_turn_kernel(AppendArgs a) {
+  turn_queries<BF16, D, 4>(a, blockIdx.x);
 }
 
 template <bool BF16, int D, int PAGE>
@@ -506,15 +555,29 @@ kq_status cache_append_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q
   // max_q consecutive tokens touch at most this many blocks, wherever they begin
   a.blocks = static_cast<int>((int64_t(b.max_q) + c.page - 2) / c.page + 1);
   a.kv_wgs = int64_t(b.batch) * a.blocks * c.kv_heads * 2;
-  const int waves = c.page / 16;
-  // a wave takes 8 heads of a token; all heads of a few tokens are spread wider, for latency
-  const int per_wave = int64_t(b.batch) * b.max_q * heads > 8192 ? kHeadsPerWave : 128 / c.head_dim;
+  // A wave takes 8 heads of a token of a long prompt, whose queries have a launch of their own; all heads of a few
+  // tokens are spread wider and go with the blocks, for latency.
+  const bool many = q_out && int64_t(b.batch) * b.max_q * heads > 8192;
+  const int waves = many ? 4 : c.page / 16;
+  const int per_wave = many ? kHeadsPerWave : 128 / c.head_dim;
   a.q_groups = heads ? (heads + per_wave - 1) / per_wave : 1;
   const int64_t per_b = (int64_t(b.max_q) * a.q_groups + waves - 1) / waves * waves;
   const int64_t q_wgs = q_out ? int64_t(b.batch) * per_b / waves : 0;
-  const int64_t wgs = a.kv_wgs + q_wgs;
-  if (wgs > int64_t(INT32_MAX))
+  if (a.kv_wgs + q_wgs > int64_t(INT32_MAX))
     return fail(KQ_EUNSUPPORTED, "kq_cache_append: batch %d with max_q %d needs too many workgroups", b.batch, b.max_q);
+  if (many) {
+    LaunchTimer timer("cache_turn_kernel", st);
+    const dim3 grid(static_cast<uint32_t>(q_wgs)), block(256);
+    if (bf16) {
+      if (c.head_dim == 64) hipLaunchKernelGGL((cache_turn_kernel<true, 64>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((cache_turn_kernel<true, 128>), grid, block, 0, st, a);
+    } else {
+      if (c.head_dim == 64) hipLaunchKernelGGL((cache_turn_kernel<false, 64>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((cache_turn_kernel<false, 128>), grid, block, 0, st, a);
+    }
+  }
+  if (const kq_status r = check_launch("cache_turn_kernel"); r != KQ_OK) return r;
+  const int64_t wgs = a.kv_wgs + (many ? 0 : q_wgs);
   if (bf16) {
     if (c.head_dim == 64) launch_append<true, 64>(a, c.page, wgs, st);
     else launch_append<true, 128>(a, c.page, wgs, st);
