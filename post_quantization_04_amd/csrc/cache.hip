@@ -20,7 +20,7 @@
 namespace kq {
 namespace {
 
-constexpr int kHeadsPerWave = 8;                       // of a long prompt's queries, all loads in flight
+constexpr int kHeadsPerWave = 16;                      // of a long prompt's queries, all loads in flight
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100: keeps 1 / scale and its sums finite
 
 struct AppendArgs {
@@ -438,27 +438,23 @@ struct ReadArgs {
   int64_t items;
 };
 
-// 16 consecutive values at out + at (8 + 8 bf16 or 4 x 4 float32).
-template <bool BF16>
-__device__ __forceinline__ void store16(void* out, int64_t at, uint4 codes, float scale) {
-  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float f[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) f[t] = float(int8_t(w[i] >> (8 * t))) * scale;
-    if (BF16) {
-      uint2 o;
-      o.x = pack_bf16(f[0], f[1]);
-      o.y = pack_bf16(f[2], f[3]);
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + at + 4 * i) = o;
-    } else {
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at + 4 * i) = make_float4(f[0], f[1], f[2], f[3]);
-    }
+// N consecutive values at out + at: 16 bytes (8 bf16, 4 float32) or half of that.
+template <bool BF16, int N>
+__device__ __forceinline__ void store_values(void* out, int64_t at, const float (&f)[N]) {
+  if constexpr (BF16) {
+    uint16_t* const p = reinterpret_cast<uint16_t*>(out) + at;
+    if constexpr (N == 8)
+      *reinterpret_cast<uint4*>(p) =
+          make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+  } else {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at) = make_float4(f[0], f[1], f[2], f[3]);
   }
 }
 
-// A wave for each 16 tokens of a head: the keys 16 channels a lane, the values two channels a lane.
+// A wave for each 16 tokens of a head. Keys: 16 bytes of output a lane, whole rows a store. Values: four channels a
+// lane of 8 (64 channels: 4) of the tokens, whole rows a store again.
 template <bool BF16, int D>
 __global__ __launch_bounds__(256) void cache_read_kernel(ReadArgs a) {
   const int lane = threadIdx.x & 63;
@@ -492,32 +488,39 @@ __global__ __launch_bounds__(256) void cache_read_kernel(ReadArgs a) {
   const int64_t row0 = int64_t(s.row0) + pos0 - first;  // row of slot 0 of the group
   if (a.out[0]) {
     const int8_t* const src = a.k + (block * page + off) * D;
-    constexpr int LR = D / 16, STEPS = 16 * LR / 64;    // lanes a row
-    uint4 c[STEPS];
-#pragma unroll
-    for (int t = 0; t < STEPS; ++t) c[t] = *reinterpret_cast<const uint4*>(src + (64 * t + lane) * 16);
+    constexpr int N = BF16 ? 8 : 4, LR = D / N, STEPS = 16 * LR / 64;   // values a lane, lanes a row
+    uint32_t c[STEPS][N / 4];
 #pragma unroll
     for (int t = 0; t < STEPS; ++t) {
-      const int slot = (64 * t + lane) / LR, d = (lane % LR) * 16;
-      if (slot >= lo && slot < hi) store16<BF16>(a.out[0], (row0 + slot) * a.ld[0] + int64_t(head) * D + d, c[t], ks);
+      const uint32_t* const at = reinterpret_cast<const uint32_t*>(src + (64 * t + lane) * N);
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) c[t][i] = at[i];
+    }
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) {
+      const int slot = (64 * t + lane) / LR, d = lane % LR * N;
+      float f[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = float(int8_t(c[t][i / 4] >> (8 * (i % 4)))) * ks;
+      if (slot >= lo && slot < hi) store_values<BF16, N>(a.out[0], (row0 + slot) * a.ld[0] + int64_t(head) * D + d, f);
     }
   }
   if (a.out[1]) {
-    constexpr int LPR = D / 2;
-    const int l = lane & (LPR - 1), hh = lane / LPR;
-    const uint4* const src = reinterpret_cast<const uint4*>(a.v + (block * page + off) * D) + 2 * l;
-    const uint4 c0 = src[0], c1 = src[1];
-    const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+    constexpr int LR = D / 4, TOK = LR / 4;               // lanes a row, tokens a lane
+    const int d = lane % LR * 4, t0 = lane / LR * TOK;
+    const int8_t* const src = a.v + (block * page + off) * D + d * 16 + t0;
+    uint32_t c[4][TOK / 4];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      if (D == 64 && (t & 1) != hh) continue;           // two rows at a time
-      if (t < lo || t >= hi) continue;
-      const float f0 = float(int8_t(w0[t >> 2] >> (8 * (t & 3)))) * vs, f1 = float(int8_t(w1[t >> 2] >> (8 * (t & 3)))) * vs;
-      const int64_t at = (row0 + t) * a.ld[1] + int64_t(head) * D + 2 * l;
-      if (BF16)
-        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out[1]) + at) = pack_bf16(f0, f1);
-      else
-        *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out[1]) + at) = make_float2(f0, f1);
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int i = 0; i < TOK / 4; ++i) c[e][i] = *reinterpret_cast<const uint32_t*>(src + 16 * e + 4 * i);
+#pragma unroll
+    for (int t = 0; t < TOK; ++t) {
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = float(int8_t(c[e][t / 4] >> (8 * (t % 4)))) * vs;
+      if (t0 + t >= lo && t0 + t < hi)
+        store_values<BF16, 4>(a.out[1], (row0 + t0 + t) * a.ld[1] + int64_t(head) * D + d, f);
     }
   }
 }
@@ -555,7 +558,7 @@ kq_status cache_append_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q
   // max_q consecutive tokens touch at most this many blocks, wherever they begin
   a.blocks = static_cast<int>((int64_t(b.max_q) + c.page - 2) / c.page + 1);
   a.kv_wgs = int64_t(b.batch) * a.blocks * c.kv_heads * 2;
-  // A wave takes 8 heads of a token of a long prompt, whose queries have a launch of their own; all heads of a few
+  // A wave takes 16 heads of a token of a long prompt, whose queries have a launch of their own (197 us with 8, 184); all heads of a few
   // tokens are spread wider and go with the blocks, for latency.
   const bool many = q_out && int64_t(b.batch) * b.max_q * heads > 8192;
   const int waves = many ? 4 : c.page / 16;
