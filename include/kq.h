@@ -498,7 +498,7 @@ typedef struct {
  *   seq_lens  device int32 [batch], each in [0, max_pages * page]
  *   q_start   device int32 [batch + 1], ascending, within [0, rows]; rows at or
  *             past q_start[batch] are neither read nor written
- *   max_q     no sequence has more than max_q rows
+ *   max_q     no sequence has more than max_q rows (a bound; one past `rows` counts as `rows`)
  *   max_pages * page < 2^31
  * What the host cannot see is checked on the device: a wrong entry sets a bit
  * of the call's info word (KQ_INFO_*) and is never followed out of bounds.
@@ -522,7 +522,7 @@ typedef struct {
  *   (a, c) -> (a cos - c sin, c cos + a sin)      (with rope) over the pairs
  *             (j, j + rot_dim/2) or, KQ_ROPE_INTERLEAVED, (2j, 2j+1), j < rot_dim/2;
  *             entries from rot_dim on pass unrotated
- * q is rounded once to its type and written to q_out. A block (page, head)
+ * q is rounded to its type (to bf16 through float32) and written to q_out. A block (page, head)
  * that takes new keys, A their largest magnitude, gets the scale
  *   s = max(s_old, A > 0 ? max(float32(A / 127), 2^-100) : 0)
  * (s_old 0 where the page's first slot is among the new tokens) and the codes

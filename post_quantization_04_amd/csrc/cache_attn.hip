@@ -141,7 +141,7 @@ struct Range {
 __device__ __forceinline__ Range chunk_range(const AttnArgs& a, const Seq& s, int i_first, int i_last, int split) {
   const int p_last = s.len - s.n + i_last, p_first = s.len - s.n + i_first;
   if (p_last < 0) return Range{0, 0, 0, 0, 1};
-  const int low = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
+  const int low = a.window > 0 ? int(max(int64_t(0), int64_t(p_first) - a.window + 1)) : 0;
   const int c = low >> 6, n = (p_last >> 6) + 1 - c;
   const int per = max((n + a.splits - 1) / a.splits, 8);   // single tokens: a chunk for each wave
   const int c0 = min(c + split * per, c + n);
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
     const float iv = vscale == 0.0f ? 0x1p48f : __builtin_amdgcn_rcpf(vscale);   // a unit of float32 off
     const int t0 = 64 * c + 16 * lk;                           // this lane's first token
     const bool cut = 64 * c + 63 > p_first || (a.window > 0 && 64 * c <= p_last - a.window);
-    const int hi = p - t0, lo = a.window > 0 ? hi - a.window : -1;  // tokens x in (lo, hi] are seen
+    const int hi = p - t0, lo = a.window > 0 && hi >= 0 ? hi - a.window : -1;  // tokens x in (lo, hi] are seen
     if (cut) {
 #pragma unroll
       for (int x = 0; x < 16; ++x) e[x >> 2][x & 3] = (x <= hi && x > lo) ? e[x >> 2][x & 3] : -INFINITY;
@@ -552,7 +552,7 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
   auto hide = [&](int c, int h, floatx16& e) {                 // scores that the row must not see
     const int z = 64 * c + 32 * h;
     if (z + 31 <= p_lo && !(a.window > 0 && z <= p_hi - a.window)) return;
-    const int hi = pos - (z + 16 * lh), lo = a.window > 0 ? hi - a.window : -(1 << 30);
+    const int hi = pos - (z + 16 * lh), lo = a.window > 0 && hi >= 0 ? hi - a.window : -1;
 #pragma unroll
     for (int x = 0; x < 16; ++x) e[x] = (x <= hi && x > lo) ? e[x] : -INFINITY;
   };
@@ -769,6 +769,11 @@ struct Plan {
   int tile_rows, tiles, splits;
 };
 
+// A window that no sequence can outgrow hides nothing.
+int effective_window(const kq_cache& c, const kq_cache_batch& b, int window) {
+  return window >= int64_t(b.max_pages) * c.page ? 0 : window;
+}
+
 Plan plan(const kq_cache& c, const kq_cache_batch& b, int heads, int window) {
   Plan p;
   const int64_t rows = int64_t(b.max_q) * (heads / c.kv_heads), heads_all = int64_t(b.batch) * c.kv_heads;
@@ -816,9 +821,8 @@ kq_status launch(const AttnArgs& a, bool prompt, hipStream_t st) {
 
 }  // namespace
 
-size_t cache_attention_workspace(const kq_cache& c, const kq_cache_batch& b, bool bf16, int64_t rows, int heads,
-                                 int window) {
-  const Plan p = plan(c, b, heads, window);
+size_t cache_attention_workspace(const kq_cache& c, const kq_cache_batch& b, int64_t rows, int heads, int window) {
+  const Plan p = plan(c, b, heads, effective_window(c, b, window));
   if (p.splits == 1) return 0;
   return size_t(rows) * heads * p.splits * (c.head_dim + 2) * sizeof(float);
 }
@@ -826,6 +830,7 @@ size_t cache_attention_workspace(const kq_cache& c, const kq_cache_batch& b, boo
 kq_status cache_attention_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q, bool bf16, int64_t rows,
                               int heads, float scale, int window, void* out, int64_t ldo, int32_t* info, void* ws,
                               hipStream_t st) {
+  window = effective_window(c, b, window);
   const Plan p = plan(c, b, heads, window);
   AttnArgs a;
   a.seq = seq_args(c, b, rows, info);

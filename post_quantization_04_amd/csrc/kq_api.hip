@@ -393,6 +393,13 @@ kq_status cache_pointers(const char* what, const kq_cache* c, const kq_cache_bat
   return KQ_OK;
 }
 
+// The batch as the kernels take it: no sequence has more rows than the call, whatever the caller's bound.
+kq_cache_batch cache_bounded(const kq_cache_batch* b, int64_t rows) {
+  kq_cache_batch r = *b;
+  r.max_q = static_cast<int32_t>(std::min<int64_t>(r.max_q, rows));
+  return r;
+}
+
 // One [rows, heads, head_dim] tensor of a cache call.
 kq_status cache_tensor(const char* what, const char* name, const void* p, int32_t dtype, int64_t rows, int64_t heads,
                        int64_t dim, int64_t ld) {
@@ -436,7 +443,7 @@ kq_status kq_cache_append(const kq_cache* cache, const kq_cache_batch* batch, co
     return fail(KQ_EINVAL, "%s: rot_dim must be a multiple of 4 up to head_dim, with rope_len >= 1 (rot_dim %d, rope_len %lld)",
                 what, rot_dim, (long long)rope_len);
   if (rows == 0 || batch->batch == 0 || batch->max_q == 0) return KQ_OK;
-  return kq::cache_append_run(*cache, *batch, {q, ldq}, {k, ldk}, {v, ldv}, dtype == KQ_BF16, rows, heads, q_norm, k_norm,
+  return kq::cache_append_run(*cache, cache_bounded(batch, rows), {q, ldq}, {k, ldk}, {v, ldv}, dtype == KQ_BF16, rows, heads, q_norm, k_norm,
                               eps, rope, rope_len, rot_dim, (flags & KQ_ROPE_INTERLEAVED) != 0, q_out, ldqo, info,
                               kq::as_stream(stream));
 }
@@ -452,7 +459,7 @@ kq_status kq_cache_read(const kq_cache* cache, const kq_cache_batch* batch, void
   if (k_out && (st = cache_tensor(what, "k_out", k_out, dtype, rows, cache->kv_heads, cache->head_dim, ldk)) != KQ_OK) return st;
   if (v_out && (st = cache_tensor(what, "v_out", v_out, dtype, rows, cache->kv_heads, cache->head_dim, ldv)) != KQ_OK) return st;
   if (rows == 0 || batch->batch == 0 || batch->max_q == 0) return KQ_OK;
-  return kq::cache_read_run(*cache, *batch, k_out, v_out, dtype == KQ_BF16, rows, ldk, ldv, info, kq::as_stream(stream));
+  return kq::cache_read_run(*cache, cache_bounded(batch, rows), k_out, v_out, dtype == KQ_BF16, rows, ldk, ldv, info, kq::as_stream(stream));
 }
 
 size_t kq_cache_attention_workspace(const kq_cache* cache, const kq_cache_batch* batch, int32_t dtype, int64_t rows,
@@ -461,7 +468,8 @@ size_t kq_cache_attention_workspace(const kq_cache* cache, const kq_cache_batch*
   if (cache_sizes("kq_cache_attention_workspace", cache, batch, rows) != KQ_OK) return bad;
   if ((dtype != KQ_BF16 && dtype != KQ_F32) || heads < 1 || heads > 65536 || heads % cache->kv_heads || window < 0) return bad;
   if (rows == 0 || batch->batch == 0 || batch->max_q == 0) return 0;
-  return kq::cache_attention_workspace(*cache, *batch, dtype == KQ_BF16, rows, heads, window);
+  if (rows * heads > INT32_MAX) return bad;
+  return kq::cache_attention_workspace(*cache, cache_bounded(batch, rows), rows, heads, window);
 }
 
 kq_status kq_cache_attention(const kq_cache* cache, const kq_cache_batch* batch, const void* q, int32_t dtype,
@@ -480,9 +488,12 @@ kq_status kq_cache_attention(const kq_cache* cache, const kq_cache_batch* batch,
   if ((st = cache_tensor(what, "out", out, dtype, rows, heads, cache->head_dim, ldo)) != KQ_OK) return st;
   if (rows > 0 && q == out) return fail(KQ_EINVAL, "%s: out must not be q", what);
   if (rows == 0 || batch->batch == 0 || batch->max_q == 0) return KQ_OK;
-  if (!ws_ok(ws, ws_bytes, kq::cache_attention_workspace(*cache, *batch, dtype == KQ_BF16, rows, heads, window))) return KQ_EINVAL;
+  if (rows * heads > INT32_MAX)
+    return fail(KQ_EUNSUPPORTED, "%s: %lld rows of %d heads", what, (long long)rows, heads);
+  const kq_cache_batch bounded = cache_bounded(batch, rows);
+  if (!ws_ok(ws, ws_bytes, kq::cache_attention_workspace(*cache, bounded, rows, heads, window))) return KQ_EINVAL;
   if (reinterpret_cast<uintptr_t>(ws) & 15) return fail(KQ_EINVAL, "%s: workspace must be 16-byte aligned", what);
-  return kq::cache_attention_run(*cache, *batch, {q, ldq}, dtype == KQ_BF16, rows, heads, scale, window, out, ldo, info, ws,
+  return kq::cache_attention_run(*cache, bounded, {q, ldq}, dtype == KQ_BF16, rows, heads, scale, window, out, ldo, info, ws,
                                  kq::as_stream(stream));
 }
 

@@ -107,8 +107,7 @@ kq_status cache_append_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q
                            int64_t ldqo, int32_t* info, hipStream_t st);
 kq_status cache_read_run(const kq_cache& c, const kq_cache_batch& b, void* k_out, void* v_out, bool bf16, int64_t rows,
                          int64_t ldk, int64_t ldv, int32_t* info, hipStream_t st);
-size_t cache_attention_workspace(const kq_cache& c, const kq_cache_batch& b, bool bf16, int64_t rows, int heads,
-                                 int window);
+size_t cache_attention_workspace(const kq_cache& c, const kq_cache_batch& b, int64_t rows, int heads, int window);
 kq_status cache_attention_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q, bool bf16, int64_t rows,
                               int heads, float scale, int window, void* out, int64_t ldo, int32_t* info, void* ws,
                               hipStream_t st);

@@ -393,6 +393,9 @@ def attention_case(seed, dtype, heads, kvh, dim, page, lens, news, *, window=0, 
     # (few workgroups, so a long context is split there too), and with one that fills the GPU
     first = max(max(news), -(-max(16 * (256 // (len(lens) * kvh) + 1), 65) // (heads // kvh)))
     for bound in (max_q, first, 8192):
+        if bound is not None and bound > rows:   # the bound counts up to the call's rows: more of them, of no sequence
+            qd = torch.cat((qd, torch.full((bound - rows, heads, dim), float("nan"), dtype=qd.dtype, device=DEV)))
+            rows = bound
         out = torch.full((rows, heads + 1, dim), 9.0, dtype=qd.dtype, device=DEV)[:, :heads]
         info = torch.zeros(1, dtype=torch.int32, device=DEV)
         b = batch_of(table, lens, q_start, bound)
@@ -400,8 +403,8 @@ def attention_case(seed, dtype, heads, kvh, dim, page, lens, news, *, window=0, 
         if w is not None and w.numel():
             w.fill_(255)                                               # NaN wherever it is read before it is written
         kq.cache_attention(dev, b, qd, out, scale=scale, window=window, info=info, ws=w)
-        got = out.float().cpu().numpy()
-        assert (got[int(q_start[-1]):] == 9.0).all()
+        assert bool((out[int(q_start[-1]):] == 9.0).all())
+        got = out[:int(q_start[-1]) + 2].float().cpu().numpy()
         check_attention(got, cache, table, lens, q_start, q, scale, window, dtype)
         told.add(int(info.item()))
     assert len(told) == 1
@@ -537,15 +540,57 @@ def test_attention_sees_no_poisoned_block_it_must_not(dtype, news):
     assert not np.isnan(got[:134]).any() and np.isnan(got[134:150]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_many_sequences(dtype):
+    """More sequences than are ordered by length (64), and exactly that many."""
+    rng = np.random.default_rng(21)
+    for n in (64, 70):
+        lens = [int(x) for x in rng.integers(0, 90, n)]
+        news = [int(rng.integers(0, x + 1)) for x in lens]
+        attention_case(22, dtype, 4, 1, 64, 16, lens, news)
+
+
+def test_bounds_far_above_the_rows():
+    """max_q is a bound: one far above the rows asks for no more work or memory than the rows."""
+    import torch
+    kq = _kq()
+    rng = np.random.default_rng(23)
+    lens, q_start, page = [300, 20], [0, 5, 6], 32
+    table, pages = tables(rng, lens, page)
+    want = filled(rng, pages, page, 2, 64)
+    dev = upload(want)
+    b = batch_of(table, lens, q_start, 2 ** 31 - 1)
+    x = rng.standard_normal((6, 8, 64)).astype(np.float32)
+    xd, q, out = to_dev(x), torch.empty((6, 4, 64), device=DEV), torch.empty((6, 4, 64), device=DEV)
+    k, v = (torch.empty((6, 2, 64), device=DEV) for _ in range(2))
+    info = torch.zeros(1, dtype=torch.int32, device=DEV)
+    kq.cache_append(dev, b, xd[:, :4], xd[:, 4:6], xd[:, 6:], q, info=info)
+    ws = kq.cache_attention_workspace(dev, b, q)
+    assert ws.numel() <= 64 * 2 ** 20
+    kq.cache_attention(dev, b, q, out, ws=ws, window=2 ** 31 - 1, info=info)
+    kq.cache_read(dev, b, k, v, info=info)
+    x64 = x.astype(np.float64)
+    kvcache.append(want, table, lens, q_start, x64[:, :4], x64[:, 4:6], x64[:, 6:])
+    check_cache(dev, want)
+    check_attention(host(out), want, table, lens, q_start, x[:, :4], 0.125, 0, "f32")
+    wk = np.concatenate([kvcache.tokens(want, table[i], lens[i] - n, lens[i])[0] for i, n in enumerate((5, 1))])
+    np.testing.assert_array_equal(host(k), wk.astype(np.float32))
+    assert int(info.item()) == 0
+
+
 def test_attention_wrong_entries_are_told():
     import torch
     kq = _kq()
     rng = np.random.default_rng(15)
     cache = filled(rng, 8, 16, 1, 64)
     dev = upload(cache)
-    q = to_dev(rng.standard_normal((20, 2, 64)).astype(np.float32))
+    q20 = to_dev(rng.standard_normal((20, 2, 64)).astype(np.float32))
 
     def run(table, lens, q_start, max_q=20):
+        q = q20
+        if max_q > 20:                           # q_start's end past these rows is not past the call's
+            q = torch.cat((q20, torch.zeros((max_q - 20, 2, 64), device=DEV)))
+            q_start = [max_q + 1 if x == 21 else x for x in q_start]
         out, info = torch.full_like(q, 9.0), torch.zeros(1, dtype=torch.int32, device=DEV)
         kq.cache_attention(dev, batch_of(table, lens, q_start, max_q), q, out, info=info)
         return host(out), int(info.item())
@@ -558,7 +603,7 @@ def test_attention_wrong_entries_are_told():
             out, info = run(table, lens, [0, 10, 20], bound)
             assert info == kq.KQ_INFO_LENGTH
             if lens[1] == -1:
-                assert not out[10:].any()
+                assert not out[10:20].any()
             np.testing.assert_array_equal(out[:10], good[:10])  # 2^31 - 1 counts as the table's 64
         for q_start in ([0, 10, 21], [-1, 10, 20], [0, 12, 10]):
             _, info = run(table, [64, 40], q_start, bound)
@@ -581,8 +626,8 @@ def test_attention_offsets_past_32_bits():
     for name in ("k", "v", "k_scale", "v_scale"):
         getattr(dev, name)[at] = to_dev(getattr(small, name))
     for new, bound in ((1, None), (40, None), (40, 8192)):
-        q = rng.standard_normal((new, 16, dim)).astype(np.float32)
-        out = torch.empty((new, 16, dim), device=DEV)
+        q = rng.standard_normal((new if bound is None else bound, 16, dim)).astype(np.float32)
+        out = torch.empty(q.shape, device=DEV)
         kq.cache_attention(dev, batch_of([far], [600], [0, new], bound), to_dev(q), out)
         check_attention(host(out), small, [[0, 1, 2, 3, 4]], [600], [0, new], q, dim ** -0.5, 0, "f32")
     k, v = torch.empty((600, kvh, dim), device=DEV), torch.empty((600, kvh, dim), device=DEV)
