@@ -196,7 +196,7 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
   {
     const int64_t at = (int64_t(s.row0) + i) * a.ldq + int64_t(hd) * D;
     float x[2 * U][8];
-    float amax = 0.0f;
+    float amax = 0.0f, odd = 0.0f;
 #pragma unroll
     for (int t = 0; t < 2 * U; ++t) {
       load8<BF16>(a.q, at + 64 * (t >> 1) + 16 * lk + 8 * (t & 1), x[t]);
@@ -204,7 +204,11 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
 #pragma unroll
     for (int t = 0; t < 2 * U; ++t)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[t][j]) < INFINITY ? fabsf(x[t][j]) : INFINITY);
+      for (int j = 0; j < 8; ++j) {
+        amax = fmaxf(amax, fabsf(x[t][j]));
+        odd = fmaf(x[t][j], 0.0f, odd);          // NaN once an entry is not finite
+      }
+    amax = odd == odd ? amax : INFINITY;
     amax = fmaxf(amax, __shfl_xor(amax, 16));
     amax = fmaxf(amax, __shfl_xor(amax, 32));
     float up;
@@ -455,14 +459,18 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
   float fq;
   {
     const int64_t at = (int64_t(s.row0) + i) * a.ldq + int64_t(head) * D + 8 * lh;
-    float amax = 0.0f;
+    float amax = 0.0f, odd = 0.0f;
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
       float x[8];
       load8<BF16>(a.q, at + 16 * t, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]) < INFINITY ? fabsf(x[j]) : INFINITY);
+      for (int j = 0; j < 8; ++j) {
+        amax = fmaxf(amax, fabsf(x[j]));
+        odd = fmaf(x[j], 0.0f, odd);             // NaN once an entry is not finite
+      }
     }
+    amax = odd == odd ? amax : INFINITY;
     amax = fmaxf(amax, __shfl_xor(amax, 32));
     float up, down;
     row_scale(amax, up, down);
