@@ -469,6 +469,8 @@ class KVCache:
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
+        global _torch
+        _torch = torch
         _need(k.dim() == 4 and v.dim() == 5, "KVCache: k is [pages, kv_heads, page, head_dim], "
                                              "v is [pages, kv_heads, page / 16, head_dim, 16]")
         pages, heads, page, dim = k.shape
@@ -518,6 +520,7 @@ class CacheBatch:
 
 
 _CACHE_DTYPES = None
+_torch = None  # set by the first KVCache: the calls below take microseconds, an import statement a few tenths of one
 
 
 def _cache_tensor(name: str, t, heads: int, cache: KVCache, rows: Optional[int] = None, dtype=None):
@@ -559,8 +562,7 @@ def _cache_info(name: str, info, cache: KVCache):
 
 def _cache_call(name: str, fn, cache: KVCache, batch: CacheBatch, args, stream) -> None:
     """fn(cache, batch, *args, stream) on the cache's device, whichever device is current."""
-    import torch
-    device = cache.device
+    torch, device = _torch, cache.device
     if device.type != "cuda" or batch.device != device:
         raise KQError(KQ_EINVAL, f"{name}: cache and batch must be on one GPU")
     if stream is None:
@@ -583,8 +585,7 @@ def cache_append(cache: KVCache, batch: CacheBatch, q, k, v, q_out=None, *, q_no
     (or None), k and v [rows, kv_heads, head_dim], bfloat16 or float32, row pitches free; q_out like q (may be q).
     q_norm, k_norm: float32 [head_dim]; rope: float32 [positions, rot_dim], cosines then sines (pipeline.rope_table);
     info: int32 device tensor for KQ_INFO_* bits, zeroed by the caller."""
-    import torch
-    name = "cache_append"
+    torch, name = _torch, "cache_append"
     dtype = _cache_dtype(name, k)
     rows, ldk = _cache_tensor("cache_append: k", k, cache.kv_heads, cache)
     _, ldv = _cache_tensor("cache_append: v", v, cache.kv_heads, cache, rows, k.dtype)
@@ -640,8 +641,7 @@ def cache_attention(cache: KVCache, batch: CacheBatch, q, out, *, scale: Optiona
                     info=None, ws=None, stream=None) -> None:
     """out <- attention of q [rows, heads, head_dim] over the cached tokens up to each row's own position (the last
     ``window`` of them with window > 0); out like q. scale defaults to head_dim^-1/2."""
-    import torch
-    name = "cache_attention"
+    torch, name = _torch, "cache_attention"
     dtype = _cache_dtype(name, q)
     heads = q.shape[1] if q.dim() == 3 else 0
     rows, ldq = _cache_tensor("cache_attention: q", q, heads, cache)
