@@ -389,7 +389,7 @@ kq_status cache_pointers(const char* what, const kq_cache* c, const kq_cache_bat
   if (!c->k || !c->v || !c->k_scale || !c->v_scale) return fail(KQ_EINVAL, "%s: NULL cache pointer", what);
   if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15)
     return fail(KQ_EINVAL, "%s: the cache's codes must be 16-byte aligned", what);
-  if (!b->table || !b->seq_lens || !b->q_start) return fail(KQ_EINVAL, "%s: NULL batch pointer", what);
+  if (b->batch > 0 && (!b->table || !b->seq_lens || !b->q_start)) return fail(KQ_EINVAL, "%s: NULL batch pointer", what);
   return KQ_OK;
 }
 
@@ -426,12 +426,12 @@ kq_status kq_cache_append(const kq_cache* cache, const kq_cache_batch* batch, co
   if (dtype != KQ_BF16 && dtype != KQ_F32) return fail(KQ_EINVAL, "%s: dtype must be KQ_BF16 or KQ_F32", what);
   if (flags & ~uint32_t(KQ_ROPE_INTERLEAVED)) return fail(KQ_EINVAL, "%s: unknown flags %u", what, flags);
   if ((st = cache_pointers(what, cache, batch)) != KQ_OK) return st;
-  if (!q != !q_out || (q && heads < 1) || heads < 0 || heads > 65536 || (!q && heads != 0))
+  if (heads < 0 || heads > 65536 || (rows > 0 && (!q != (heads == 0) || !q_out != (heads == 0))))
     return fail(KQ_EINVAL, "%s: q and q_out come together, with heads >= 1, or both NULL with heads 0", what);
-  if (q) {
+  if (heads > 0) {
     if ((st = cache_tensor(what, "q", q, dtype, rows, heads, cache->head_dim, ldq)) != KQ_OK) return st;
     if ((st = cache_tensor(what, "q_out", q_out, dtype, rows, heads, cache->head_dim, ldqo)) != KQ_OK) return st;
-    if (q == q_out && ldq != ldqo) return fail(KQ_EINVAL, "%s: q in place needs equal pitches", what);
+    if (rows > 0 && q == q_out && ldq != ldqo) return fail(KQ_EINVAL, "%s: q in place needs equal pitches", what);
   }
   if ((st = cache_tensor(what, "k", k, dtype, rows, cache->kv_heads, cache->head_dim, ldk)) != KQ_OK) return st;
   if ((st = cache_tensor(what, "v", v, dtype, rows, cache->kv_heads, cache->head_dim, ldv)) != KQ_OK) return st;

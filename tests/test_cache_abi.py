@@ -148,6 +148,18 @@ def test_nothing_to_do_is_ok(L):
 # ---- the binding's checks --------------------------------------------------------------------------------------
 
 
+def test_empty_tensors_are_nothing_to_do(L):
+    """An empty tensor's pointer is NULL: no rows, or no sequences, is no error."""
+    c, b = _cache(), _batch()
+    assert L.kq_cache_append(ctypes.byref(c), ctypes.byref(b), None, None, None, kq.KQ_BF16, 0, 32, 4096, 1024, 1024,
+                             None, None, 1e-6, None, 0, 0, 0, None, 4096, None, None) == kq.KQ_OK
+    none = _batch(batch=0, table=None, seq_lens=None)
+    for fn, args in _calls(L):
+        assert fn(ctypes.byref(c), ctypes.byref(none), *args) == kq.KQ_OK
+    assert L.kq_cache_append(ctypes.byref(c), ctypes.byref(b), *_with(APPEND, 0, None)) == kq.KQ_EINVAL
+    assert L.kq_cache_append(ctypes.byref(c), ctypes.byref(b), *_with(APPEND, 16, None)) == kq.KQ_EINVAL
+
+
 def _tensors(rows=3, heads=4, kv_heads=2, dim=64, page=16, pages=6):
     import torch
     cache = kq.KVCache.allocate(pages, page, kv_heads, dim, "cpu")
