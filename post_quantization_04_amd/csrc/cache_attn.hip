@@ -29,9 +29,13 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTokenWaves = 8;          // waves that share a workgroup's range of the context
-constexpr float kNoToken = -1.0e30f;   // running maximum before the first token (finite: no inf - inf)
+constexpr float kNoToken = -3.0e38f;   // running maximum before the first token (finite: no inf - inf)
 constexpr float kZeroScale = -48.0f;   // log2 taken for a value scale of 0: any finite one (its codes are 0)
 constexpr float kWeightExp = 14.0f;    // weights are held times 2^14, so that float16 keeps small ones
+// Exponents are one fused multiply-add from the scores, e f + (log2 s_v - m), exact but for the rounding of m. Where
+// m is larger than this, that rounding counts (2^-2 here, and a weight of 2^2 would pass float16's range): the
+// exponent is then rounded as m is, before m is taken off, so that the largest is 0.
+constexpr float kFarMax = 4194304.0f;
 
 struct AttnArgs {
   SeqArgs seq;
@@ -282,7 +286,7 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
     if constexpr (more) load_keys();
     lost |= !known;
     const float kscale = known ? ks : NAN, vscale = known ? vs : NAN;
-    const float f = kscale * qf;                               // scores to base-2 exponents
+    float f = kscale * qf;                                     // scores to base-2 exponents
     const float lv = vscale > 0.0f ? __log2f(vscale) : vscale == 0.0f ? kZeroScale : NAN;
     const float iv = vscale == 0.0f ? 0x1p48f : __builtin_amdgcn_rcpf(vscale);   // a unit of float32 off
     const int t0 = 64 * c + 16 * lk;                           // this lane's first token
@@ -304,7 +308,13 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
     l *= fall;
 #pragma unroll
     for (int t = 0; t < DT; ++t) o[t] *= fall;
-    const float shift = lv - m + kWeightExp;
+    float shift = lv - m + kWeightExp;
+    if (__any(fabsf(m) > kFarMax)) {
+#pragma unroll
+      for (int x = 0; x < 16; ++x) e[x >> 2][x & 3] = fmaf(e[x >> 2][x & 3], f, lv) - m;
+      f = 1.0f;
+      shift = kWeightExp;
+    }
     float sum = 0.0f;
     float w[16];
 #pragma unroll
@@ -403,8 +413,8 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
 
 // A block's scales as the weights use them, finite where they multiply scores. A NaN (a poisoned block, a bad
 // page) becomes a weight of 2^100 for whoever sees a token of it, and a NaN in their sum.
-struct BlockScale {
-  float ks, lv, iv, unused;
+struct alignas(16) BlockScale {
+  float ks, lv, iv;
 };
 
 __device__ __forceinline__ BlockScale block_scale(float ks, float vs) {
@@ -413,7 +423,6 @@ __device__ __forceinline__ BlockScale block_scale(float ks, float vs) {
   r.ks = bad ? 0x1p-100f : ks > 0.0f ? ks : 1.0f;            // 0: the codes are 0, so any factor will do
   r.lv = bad ? 100.0f : vs > 0.0f ? __log2f(vs) : kZeroScale;
   r.iv = bad ? NAN : vs > 0.0f ? __builtin_amdgcn_rcpf(vs) : 0x1p48f;   // the reciprocal a unit of float32 off
-  r.unused = 0.0f;
   return r;
 }
 
@@ -564,8 +573,8 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
 #pragma unroll
     for (int x = 0; x < 16; ++x) e[x] = (x <= hi && x > lo) ? e[x] : -INFINITY;
   };
-  // The running maximum takes the scores of a half in; f is what turns them into exponents.
-  auto raise = [&](const floatx16& e, float f, float lv) {
+  // The running maximum takes the scores of a half in; f and the shift it returns turn them into weights' exponents.
+  auto raise = [&](floatx16& e, float& f, float lv) {
     float x0 = e[0], x1 = e[1];
 #pragma unroll
     for (int x = 2; x < 16; x += 2) {
@@ -580,16 +589,26 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t] *= fall;
     }
+    float shift = lv - m + kExp;
+    if (__any(fabsf(m) > kFarMax)) {             // no farther above 0 than the maximum may lag, whatever m + kLag was
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const float t = fmaf(e[x], f, lv) - m;
+        e[x] = t > kLag ? kLag : t;              // a NaN stays
+      }
+      f = 1.0f;
+      shift = kExp;
+    }
+    return shift;
   };
   auto factor = [&](const BlockScale& bs) {
     return fmaxf(bs.ks * fq, 1e-37f);            // above 0, so that a hidden score stays -inf
   };
-  // Half h of tile c from its scores e on: the weights alternate with the products of the queries and the next
+  // Half h of a tile from its scores e on: the weights alternate with the products of the queries and the next
   // half's keys (to en), then the products with the values with the unpacking of chunk `part` of a later tile.
   // A wave's MFMAs and vector instructions overlap only where they alternate.
-  auto half_body = [&](int c, int h, const BlockScale& bs, float f, const floatx16& e, int slot, int kslot, floatx16& en,
+  auto half_body = [&](int h, float iv, float f, float shift, const floatx16& e, int slot, int kslot, floatx16& en,
                        auto&& unpack) {
-    const float shift = bs.lv - m + kExp;
     float sum = 0.0f;
     half8 pf[P][2];
 #pragma unroll
@@ -611,7 +630,7 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
         }
       }
     }
-    l = sum > 0.0f ? fmaf(sum, bs.iv, l) : l;    // a poisoned block that the row does not see stays out of it
+    l = sum > 0.0f ? fmaf(sum, iv, l) : l;    // a poisoned block that the row does not see stays out of it
     unpack();
     const half8* const vr = sv + slot * VB + vat + 4 * h;
 #pragma unroll
@@ -655,13 +674,13 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
       look(c + 4);
     } else {
       const BlockScale b0 = sc[t0 & 3][lh], b1 = sc[t0 & 3][2 + lh];
-      const float f0 = factor(b0), f1 = factor(b1);
+      float f0 = factor(b0), f1 = factor(b1);
       hide(c, 0, e0);
-      raise(e0, f0, b0.lv);
-      half_body(c, 0, b0, f0, e0, now, now, e1, [&] { stage(far, 0, CH / 2); });
+      const float shift0 = raise(e0, f0, b0.lv);
+      half_body(0, b0.iv, f0, shift0, e0, now, now, e1, [&] { stage(far, 0, CH / 2); });
       hide(c, 1, e1);
-      raise(e1, f1, b1.lv);
-      half_body(c, 1, b1, f1, e1, now, next, e0, [&] {
+      const float shift1 = raise(e1, f1, b1.lv);
+      half_body(1, b1.iv, f1, shift1, e1, now, next, e0, [&] {
         stage(far, CH / 2, CH);
         fetch(c + 3);
         look(c + 4);

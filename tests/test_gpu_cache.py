@@ -513,6 +513,57 @@ def test_attention_query_sizes(dtype, news):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 27, 2.0 ** 63, -2.0 ** 27, -2.0 ** 45, -2.0 ** 105])
+@pytest.mark.parametrize("bound", [150, 2000])
+def test_attention_scores_beyond_their_rounding(dtype, size, bound):
+    """Scores so large that a unit of their float32 rounding passes the exponential's: the token of the largest score
+    has all of the weight. Its weight is a power of two, so the output is its value, off by the reciprocals of the
+    scale and of the sum, their product's sums and the last product (2^-23 and three times 2^-24: below 2^-21), and
+    by bf16's 2^-8. Bound 150: rows in tiles of 16; 2000: of 256."""
+    import torch
+    kq = _kq()
+    rng = np.random.default_rng(31)
+    n, heads = 150, 4
+    table, pages = tables(rng, [n], 16)
+    cache = filled(rng, pages, 16, 1, 128)
+    order = rng.permutation(n)                 # a score's size: 64 (2 + order) times the query's entry
+    for t in range(n):
+        at = cache.k[table[0][t // 16], 0, t % 16]
+        at[:64] = 1 + order[t] // 2
+        at[64:] = 1 + (order[t] + 1) // 2
+    cache.k_scale[:] = 1.0
+    q = _dev(np.full((max(bound, n), heads, 128), size), dtype)
+    out = torch.zeros_like(q)
+    kq.cache_attention(upload(cache), batch_of(table, [n], [0, n], bound), q, out, scale=0.5)
+    got = out[:n].float().cpu().numpy().astype(np.float64)
+    for i in range(n):
+        t = max(range(i + 1), key=lambda x: order[x] * np.sign(size))
+        page, slot = table[0][t // 16], t % 16
+        want = cache.v[page, 0, slot // 16, :, slot % 16].astype(np.float64) * np.float64(cache.v_scale[page, 0])
+        tol = np.abs(want) * (2.0 ** -21 + (2.0 ** -8 if dtype == "bf16" else 0.0))
+        assert (np.abs(got[i] - want) <= tol).all(), (i, t)
+
+
+def test_calls_with_nothing_to_do():
+    """No rows, or no sequences: empty tensors pass through the binding and nothing is written."""
+    import torch
+    kq = _kq()
+    dev = kq.KVCache.allocate(4, 16, 2, 64, DEV)
+    before = [t.clone() for t in (dev.k, dev.v, dev.k_scale, dev.v_scale)]
+    none = kq.CacheBatch(torch.zeros((0, 3), dtype=torch.int32, device=DEV), torch.zeros(0, dtype=torch.int32, device=DEV),
+                         torch.zeros(1, dtype=torch.int32, device=DEV), 5)
+    for rows, batch in ((0, batch_of([[0, 1]], [7], [0, 0])), (0, none), (3, none)):
+        q, kv = torch.ones((rows, 4, 64), device=DEV), torch.ones((rows, 2, 64), device=DEV)
+        out, back = torch.full_like(q, 9.0), torch.full_like(kv, 9.0)
+        kq.cache_append(dev, batch, q, kv, kv, out)
+        kq.cache_append(dev, batch, None, kv, kv)
+        kq.cache_attention(dev, batch, q, out)
+        kq.cache_read(dev, batch, back, None)
+        assert bool((out == 9.0).all()) and bool((back == 9.0).all())
+    assert all(torch.equal(a, b) for a, b in zip(before, (dev.k, dev.v, dev.k_scale, dev.v_scale)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("news", [[1], [3], [150]])
 def test_attention_sees_no_poisoned_block_it_must_not(dtype, news):
     """A NaN scale reaches the rows that see its block and no others, also where the block shares a tile with what
