@@ -154,12 +154,14 @@ def attention_step(x, qkv, o, cache: KVCache, batch: CacheBatch, heads: int, *, 
     ``s_x`` and ``rot_in`` belong to q, k and v, ``o_s_x`` and ``o_rot_in`` to o. Returns o's y. The values in
     qkv's q are replaced by the rotated queries. ``ws`` (from ``attention_step_workspace``) and the layers' y make
     the step free of allocations, so that it can be captured into a graph."""
+    import torch
     rows, dim = x.shape[0], cache.head_dim
     y_q, y_k, y_v = (layer[5] for layer in qkv)
     _need(y_q.shape == (rows, heads * dim) and y_k.shape == y_v.shape == (rows, cache.kv_heads * dim),
           "attention_step: the layers' y do not match heads, kv_heads and head_dim")
     if ws is None:
-        ws = attention_step_workspace(x, qkv, o, cache, batch, heads)
+        with torch.cuda.stream(stream):      # memory of the stream that uses it (None: the current one)
+            ws = attention_step_workspace(x, qkv, o, cache, batch, heads)
     q = y_q.view(rows, heads, dim)
     decode_matvec_group(qkv, bits, group, s_x, rot_in, x, ws=ws.qkv, stream=stream)
     cache_append(cache, batch, q, y_k.view(rows, cache.kv_heads, dim), y_v.view(rows, cache.kv_heads, dim), q,

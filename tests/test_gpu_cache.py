@@ -778,10 +778,10 @@ def test_graph_replays_with_new_contents():
 # ---- together, as they are used -----------------------------------------------------------------------------------
 
 
-@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("graph", [False, True, "stream"])
 def test_attention_step_on_quantized_weights(graph):
     """A prompt through append and attention, then single tokens through pipeline.attention_step (packed q, k, v, o
-    layers, cache, attention), eager or as one captured graph, against the oracle fed with the same steps.
+    layers, cache, attention), eager, as one captured graph or on a stream of its own, against the oracle fed with the same steps.
 
     The oracle's own chain feeds each step: decode matvec (2e-5 of the norm, as its own tests hold), then the cache.
     A key or value entry off by 2e-5 of its row can take another code, one step of its block's scale; so the step is
@@ -836,12 +836,13 @@ def test_attention_step_on_quantized_weights(graph):
     ws = pipeline.attention_step_workspace(xin, layers[:3], layers[3], dev, step, heads)
     s_xd, s_xod, qwd, kwd, rd = to_dev(s_x), to_dev(s_xo), to_dev(qw), to_dev(kw), rope.to(DEV)
 
-    def run():
+    def run(**kw):
+        kw = kw or dict(ws=ws)
         return pipeline.attention_step(xin, layers[:3], layers[3], dev, step, heads, bits=bits, group=group, s_x=s_xd,
-                                       rot_in=dri.rot, o_s_x=s_xod, o_rot_in=drio.rot, q_norm=qwd, k_norm=kwd, rope=rd, ws=ws)
+                                       rot_in=dri.rot, o_s_x=s_xod, o_rot_in=drio.rot, q_norm=qwd, k_norm=kwd, rope=rd, **kw)
 
     g = None
-    if graph:
+    if graph is True:
         saved = [t.clone() for t in (dev.k, dev.v, dev.k_scale, dev.v_scale)]
         run()
         g = torch.cuda.CUDAGraph()
@@ -863,6 +864,15 @@ def test_attention_step_on_quantized_weights(graph):
         y = layers[3][5]
         if g is not None:
             g.replay()
+        elif graph:
+            torch.cuda.synchronize()
+            first = run(stream=torch.cuda.Stream())                # buffers of its own
+            torch.cuda.synchronize()
+            first = first.clone()
+            torch.cuda.synchronize()
+            y = run(stream=torch.cuda.Stream(), ws=ws)             # the same token in the same place: the same cache
+            torch.cuda.synchronize()
+            assert torch.equal(first, y)
         else:
             y = run()
         qkv = [host(r).astype(np.float64).reshape(2, -1, dim) for r in ref]
