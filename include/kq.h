@@ -539,8 +539,8 @@ typedef struct {
  *   info     device int32 or NULL: KQ_INFO_* bits are or-ed in; the caller sets it to 0 first
  * A token whose position is negative (fewer tokens in the cache than rows) or
  * past the table of rotations reads as NaN in q_out; the former is not stored.
- * A token of a bad page is not stored. Pages that the call writes belong to
- * one sequence each. Norm, rotation and rounding run in float64, so that codes
+ * A token of a bad page is not stored. A page that the call writes stands once
+ * in one sequence's table (full pages may be shared). Norm, rotation and rounding run in float64, so that codes
  * do not depend on the order of operations.
  */
 kq_status kq_cache_append(const kq_cache* cache, const kq_cache_batch* batch, const void* q, const void* k,
@@ -583,7 +583,8 @@ kq_status kq_cache_read(const kq_cache* cache, const kq_cache_batch* batch, void
  *   scale    finite and > 0; window >= 0
  *   info     as kq_cache_append (rows past max_q of a sequence are left as they were)
  *   ws       kq_cache_attention_workspace bytes; calls sharing it must not overlap.
- * Tokens of a bad page count as NaN. Sums have a fixed order (deterministic).
+ * Tokens of a bad page count as NaN, and so do scores (scale q . k) past
+ * float32's range. Sums have a fixed order (deterministic).
  */
 kq_status kq_cache_attention(const kq_cache* cache, const kq_cache_batch* batch, const void* q, int32_t dtype,
                              int64_t rows, int32_t heads, int64_t ldq, float scale, int32_t window, void* out,

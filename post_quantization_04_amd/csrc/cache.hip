@@ -558,7 +558,8 @@ kq_status cache_append_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q
   // max_q consecutive tokens touch at most this many blocks, wherever they begin
   a.blocks = static_cast<int>((int64_t(b.max_q) + c.page - 2) / c.page + 1);
   a.kv_wgs = int64_t(b.batch) * a.blocks * c.kv_heads * 2;
-  // A wave takes 16 heads of a token of a long prompt, whose queries have a launch of their own (197 us with 8, 184); all heads of a few
+  // A wave takes 16 heads of a token of a long prompt, whose queries have a launch of their own (three prompts of up
+  // to 8192 tokens, 32 over 8 heads, the whole call: 197 us with 8 heads a wave, 184 with 16); all heads of a few
   // tokens are spread wider and go with the blocks, for latency.
   const bool many = q_out && int64_t(b.batch) * b.max_q * heads > 8192;
   const int waves = many ? 4 : c.page / 16;
@@ -578,8 +579,8 @@ kq_status cache_append_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q
       if (c.head_dim == 64) hipLaunchKernelGGL((cache_turn_kernel<false, 64>), grid, block, 0, st, a);
       else hipLaunchKernelGGL((cache_turn_kernel<false, 128>), grid, block, 0, st, a);
     }
+    if (const kq_status r = check_launch("cache_turn_kernel"); r != KQ_OK) return r;
   }
-  if (const kq_status r = check_launch("cache_turn_kernel"); r != KQ_OK) return r;
   const int64_t wgs = a.kv_wgs + (many ? 0 : q_wgs);
   if (bf16) {
     if (c.head_dim == 64) launch_append<true, 64>(a, c.page, wgs, st);
