@@ -42,7 +42,8 @@ struct AppendArgs {
   int heads, kvh;
   int blocks;             // blocks a sequence's new tokens can touch
   int batch;
-  int64_t kv_wgs;         // workgroups before the queries'
+  int64_t kv_wgs;         // workgroups that take blocks; the others take queries
+  int in_turn;            // spread over the grid, else the blocks first
   int q_groups;           // head groups of a token in the query part
 };
 
@@ -371,7 +372,13 @@ template <bool BF16, int D, int PAGE>
 __global__ __launch_bounds__(PAGE * 4) void cache_append_kernel(AppendArgs a) {
   constexpr int SL = D / 8, WAVES = PAGE / 16;
   int64_t id = blockIdx.x;
-  if (id < a.kv_wgs) {
+  bool block = id < a.kv_wgs;
+  if (a.in_turn) {                   // of workgroups 0 .. x, floor((x + 1) kv_wgs / all) are blocks
+    const int64_t at = id * a.kv_wgs, all = gridDim.x;
+    id = at / all;
+    block = at - id * all + a.kv_wgs >= all;
+  }
+  if (block) {
     const int side = id & 1;
     id >>= 1;
     const int head = id % a.kvh;
@@ -396,13 +403,7 @@ __global__ __launch_bounds__(PAGE * 4) void cache_append_kernel(AppendArgs a) {
     }
     return;
   }
-  turn_queries<BF16, D, WAVES>(a, id - a.kv_wgs);
-}
-
-// The queries of many tokens, on their own: the blocks' kernel needs twice the registers.
-template <bool BF16, int D>
-__global__ __launch_bounds__(256) void cache_turn_kernel(AppendArgs a) {
-  turn_queries<BF16, D, 4>(a, blockIdx.x);
+  turn_queries<BF16, D, WAVES>(a, blockIdx.x - (a.in_turn ? id : a.kv_wgs));
 }
 
 template <bool BF16, int D, int PAGE>
@@ -558,30 +559,20 @@ kq_status cache_append_run(const kq_cache& c, const kq_cache_batch& b, CacheIn q
   // max_q consecutive tokens touch at most this many blocks, wherever they begin
   a.blocks = static_cast<int>((int64_t(b.max_q) + c.page - 2) / c.page + 1);
   a.kv_wgs = int64_t(b.batch) * a.blocks * c.kv_heads * 2;
-  // A wave takes 16 heads of a token of a long prompt, whose queries have a launch of their own (three prompts of up
-  // to 8192 tokens, 32 over 8 heads, the whole call: 197 us with 8 heads a wave, 184 with 16); all heads of a few
-  // tokens are spread wider and go with the blocks, for latency.
-  const bool many = q_out && int64_t(b.batch) * b.max_q * heads > 8192;
-  const int waves = many ? 4 : c.page / 16;
+  // All heads of a few tokens are spread over waves, for latency, and blocks, which take longer, start first; a wave
+  // takes 16 heads of a token of many, and as those wait for memory where blocks wait for arithmetic, their workgroups
+  // run side by side (three prompts of up to 8192 tokens, 32 over 8 heads: 87 us for the queries alone and 102 for
+  // the blocks, 172 together; 64 single tokens take 22.1 us with the blocks first and 22.8 in turn).
+  const bool many = int64_t(b.batch) * b.max_q * heads > 8192;
+  a.in_turn = many;
+  const int waves = c.page / 16;
   const int per_wave = many ? kHeadsPerWave : 128 / c.head_dim;
   a.q_groups = heads ? (heads + per_wave - 1) / per_wave : 1;
   const int64_t per_b = (int64_t(b.max_q) * a.q_groups + waves - 1) / waves * waves;
   const int64_t q_wgs = q_out ? int64_t(b.batch) * per_b / waves : 0;
   if (a.kv_wgs + q_wgs > int64_t(INT32_MAX))
     return fail(KQ_EUNSUPPORTED, "kq_cache_append: batch %d with max_q %d needs too many workgroups", b.batch, b.max_q);
-  if (many) {
-    LaunchTimer timer("cache_turn_kernel", st);
-    const dim3 grid(static_cast<uint32_t>(q_wgs)), block(256);
-    if (bf16) {
-      if (c.head_dim == 64) hipLaunchKernelGGL((cache_turn_kernel<true, 64>), grid, block, 0, st, a);
-      else hipLaunchKernelGGL((cache_turn_kernel<true, 128>), grid, block, 0, st, a);
-    } else {
-      if (c.head_dim == 64) hipLaunchKernelGGL((cache_turn_kernel<false, 64>), grid, block, 0, st, a);
-      else hipLaunchKernelGGL((cache_turn_kernel<false, 128>), grid, block, 0, st, a);
-    }
-    if (const kq_status r = check_launch("cache_turn_kernel"); r != KQ_OK) return r;
-  }
-  const int64_t wgs = a.kv_wgs + (many ? 0 : q_wgs);
+  const int64_t wgs = a.kv_wgs + q_wgs;
   if (bf16) {
     if (c.head_dim == 64) launch_append<true, 64>(a, c.page, wgs, st);
     else launch_append<true, 128>(a, c.page, wgs, st);
