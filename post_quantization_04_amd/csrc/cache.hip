@@ -9,6 +9,10 @@
 // 16-byte store for each of its channels. Queries need no scale and go to workgroups of their
 // own, a wave for each token and group of heads.
 //
+// Three prompts of up to 8192 tokens, 32 over 8 heads, bf16 (554 MB): 172 us, 3.2 TB/s; all in
+// float32 it would be 157. Few tokens are latency: table entry, old scale, row, norm's sum, the
+// block's maximum and the code follow from one another (one token 3.9 us, 64 of them 12.1).
+//
 // Norm and rotation are float64, and so is the division where float32 cannot tell the code: in
 // float32 alone they end within 1e-5 of a step of a rounding border for one entry in 10^5, whose
 // code would then depend on the order of operations.
@@ -455,7 +459,8 @@ __device__ __forceinline__ void store_values(void* out, int64_t at, const float 
 }
 
 // A wave for each 16 tokens of a head. Keys: 16 bytes of output a lane, whole rows a store. Values: four channels a
-// lane of 8 (64 channels: 4) of the tokens, whole rows a store again.
+// lane of 8 (64 channels: 4) of the tokens, whole rows a store again. Bound by HBM: 131072 tokens of 8 heads to bf16
+// (805 MB) 144 to 157 us, 5.1 to 5.6 TB/s, a copy's rate; stores of single values took 191.
 template <bool BF16, int D>
 __global__ __launch_bounds__(256) void cache_read_kernel(ReadArgs a) {
   const int lane = threadIdx.x & 63;

@@ -12,8 +12,9 @@
 // row of q is first multiplied by the power of two that takes its largest entry to [2^14, 2^15):
 // a bf16 entry is then exact (entries 2^-38 of the row's largest are dropped), a float32 entry is
 // a sum of two float16 pieces, off by 2^-22 of itself, a float32 sum's own error over 64 terms or
-// more. Weights are scaled by 2^14 and rounded to float16 (2^-11, against the 2^-8 of a bf16
-// output), for float32 outputs to two pieces. Maxima, sums and accumulators are float32.
+// more. Weights are held times 2^14 and rounded to float16 (2^-11, against the 2^-8 of a bf16
+// output), for float32 outputs to two pieces; in bf16 prompts m may lag by 2^4 and they are held
+// times 2^11. Maxima, sums and accumulators are float32.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -164,6 +165,12 @@ __device__ __forceinline__ Range chunk_range(const AttnArgs& a, const Seq& s, in
 // cache block, and they are its operand of O^T = V^T P^T, whose other operand is 16 codes of one
 // channel: one 16-byte load. Channels are permuted likewise so that a key row's loads are 16
 // bytes a lane.
+//
+// Bound by HBM where the context is long: 64 tokens over up to 8191, 32 heads each (2.6 GB of
+// codes), 467 us, 5.6 TB/s; one token over 131070, 64 over 8 heads (268 MB), 51 us, and 4 to join
+// its parts. Short ones are latency: 300 tokens, 8.0 us, of which an empty launch is about 2.
+// Eight waves a workgroup, not four: the join in LDS is cheaper than twice the parts to join
+// from memory, and two workgroups a CU keep 32 KB of loads in flight each.
 // ---------------------------------------------------------------------------
 template <bool BF16, int D>
 __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnArgs a) {
@@ -399,7 +406,8 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
 //
 // A workgroup takes 256 rows of one sequence and head, eight waves of 32, and walks the context in tiles of 64
 // tokens. The codes of a tile are loaded and unpacked to float16 once a workgroup, into LDS, three tiles deep:
-// unpacking takes five vector instructions for four codes and is the cost that many rows have to share.
+// unpacking takes five vector instructions for four codes and is the cost that many rows have to share. Where 256 rows
+// a workgroup would leave CUs idle it takes 128, and two waves share 32 rows by halves of each tile.
 //
 // What bounds it is the SIMDs' vector issue, not the matrix pipe (measured on an 8192-token prompt over 32 heads):
 // a 32 x 32 x 16 MFMA keeps the matrix pipe busy for 32 cycles and the issue port for about 12 of them, an
@@ -426,9 +434,10 @@ __device__ __forceinline__ BlockScale block_scale(float ks, float vs) {
   return r;
 }
 
-template <bool BF16, int D>
+template <bool BF16, int D, int ROWS>
 __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
-  constexpr int NT = 512, ROWS = 256;
+  constexpr int NT = 512, GROUPS = ROWS / 32;    // groups of rows
+  constexpr bool PAIRS = GROUPS < 8;             // two waves share a group's rows, each takes half of a tile's tokens
   constexpr int KS = D / 16, DT = D / 32;        // MFMA steps over channels, 32-channel output tiles
   // LDS rows in 16-byte units, of an odd number of them so that lanes reading one unit of consecutive rows meet
   // different banks, and every step's address is a constant away from the lane's first. Keys: the token of the
@@ -459,7 +468,8 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
   if (split >= rg.parts) return;
 
   // this wave's rows, a lane's row and its position
-  const int w0 = tile * ROWS + wave * 32;
+  const int wh = PAIRS ? wave / GROUPS : 0;      // this wave's half of the tokens
+  const int w0 = tile * ROWS + (wave & (GROUPS - 1)) * 32;
   const int p_hi = w0 < nrows ? first + (min(w0 + 32, nrows) - 1) / a.g : -1, p_lo = first + min(w0, nrows - 1) / a.g;
   const int r = min(w0 + lq, nrows - 1);
   const int i = r / a.g, head = kh * a.g + (r - i * a.g);
@@ -559,7 +569,7 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
   float m = kNoToken, l = 0.0f;
 #pragma unroll
   for (int t = 0; t < DT; ++t) o[t] = floatx16{};
-  const int kat = lq * KP + lh, vat = lq * VP + 2 * lh;
+  const int kat = (lq + 32 * wh) * KP + lh, vat = lq * VP + 2 * lh + 4 * wh;
   // Scores of half h of the tile in a slot: e[x] of this lane belongs to token 64 c + 32 h + 16 lh + x.
   auto key_step = [&](int slot, int h, int t, floatx16& e) {
     const half8 kf = (sk + slot * KB + kat)[h * 32 * KP + 2 * t];
@@ -604,16 +614,16 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
   auto factor = [&](const BlockScale& bs) {
     return fmaxf(bs.ks * fq, 1e-37f);            // above 0, so that a hidden score stays -inf
   };
-  // Half h of a tile from its scores e on: the weights alternate with the products of the queries and the next
-  // half's keys (to en), then the products with the values with the unpacking of chunk `part` of a later tile.
+  // Half h of a tile from its scores e on: the weights alternate with the products of the queries and half hn's
+  // keys, the next (to en), then the products with the values with the unpacking of chunk `part` of a later tile.
   // A wave's MFMAs and vector instructions overlap only where they alternate.
-  auto half_body = [&](int h, float iv, float f, float shift, const floatx16& e, int slot, int kslot, floatx16& en,
+  auto half_body = [&](int h, float iv, float f, float shift, const floatx16& e, int slot, int kslot, int hn, floatx16& en,
                        auto&& unpack) {
     float sum = 0.0f;
     half8 pf[P][2];
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
-      key_step(kslot, h ^ 1, t, en);
+      key_step(kslot, hn, t, en);
       constexpr int PER = 16 / KS;               // weights between two steps
 #pragma unroll
       for (int x = t * PER; x < (t + 1) * PER; x += 2) {
@@ -673,18 +683,27 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
       fetch(c + 3);
       look(c + 4);
     } else {
-      const BlockScale b0 = sc[t0 & 3][lh], b1 = sc[t0 & 3][2 + lh];
+      const BlockScale b0 = sc[t0 & 3][2 * wh + lh], b1 = sc[t0 & 3][2 + lh];
       float f0 = factor(b0), f1 = factor(b1);
-      hide(c, 0, e0);
+      hide(c, wh, e0);
       const float shift0 = raise(e0, f0, b0.lv);
-      half_body(0, b0.iv, f0, shift0, e0, now, now, e1, [&] { stage(far, 0, CH / 2); });
-      hide(c, 1, e1);
-      const float shift1 = raise(e1, f1, b1.lv);
-      half_body(1, b1.iv, f1, shift1, e1, now, next, e0, [&] {
-        stage(far, CH / 2, CH);
-        fetch(c + 3);
-        look(c + 4);
-      });
+      if constexpr (PAIRS) {
+        half_body(0, b0.iv, f0, shift0, e0, now, next, 0, e1, [&] {
+          stage(far, 0, CH);
+          fetch(c + 3);
+          look(c + 4);
+        });
+        e0 = e1;
+      } else {
+        half_body(0, b0.iv, f0, shift0, e0, now, now, 1, e1, [&] { stage(far, 0, CH / 2); });
+        hide(c, 1, e1);
+        const float shift1 = raise(e1, f1, b1.lv);
+        half_body(1, b1.iv, f1, shift1, e1, now, next, 0, e0, [&] {
+          stage(far, CH / 2, CH);
+          fetch(c + 3);
+          look(c + 4);
+        });
+      }
     }
     if (((t0 + 2) & 7) == wave) stage_s((t0 + 2) & 3);
     if (((t0 + 3) & 7) == wave) fetch_s();
@@ -697,6 +716,29 @@ __global__ __launch_bounds__(512, 2) void cache_prompt_kernel(AttnArgs a) {
   }
   if (lost) report(a.seq.info, KQ_INFO_PAGE);
   l += __shfl_xor(l, 32);
+  if constexpr (PAIRS) {                         // the second wave of a pair hands its sums over, where the tiles were
+    constexpr int N = DT / 2 * 1024 + 128;       // half of them in either array, and m and l
+    static_assert(GROUPS * N * sizeof(float) <= std::min(sizeof(sk), sizeof(sv)), "a pair's sums do not fit");
+    const int at = (wave & (GROUPS - 1)) * N + lane;
+    float* const po[2] = {reinterpret_cast<float*>(sk) + at, reinterpret_cast<float*>(sv) + at};
+    if (wh) {
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) po[t & 1][(8 * (t & ~1) + x) * 64] = o[t][x];
+      po[0][DT / 2 * 1024] = m;
+      po[0][DT / 2 * 1024 + 64] = l;
+    }
+    __syncthreads();
+    if (wh) return;
+    const float m1 = po[0][DT / 2 * 1024], mn = fmaxf(m, m1), f0 = exp2_raw(m - mn), f1 = exp2_raw(m1 - mn);
+    m = mn;
+    l = l * f0 + po[0][DT / 2 * 1024 + 64] * f1;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[t][x] = o[t][x] * f0 + po[t & 1][(8 * (t & ~1) + x) * 64] * f1;
+  }
   if (w0 + lq >= nrows) return;
   const int64_t row = int64_t(s.row0) + i;
   if (pos < 0) {                                 // sees nothing, whatever its query holds
@@ -808,16 +850,22 @@ Plan plan(const kq_cache& c, const kq_cache_batch& b, int heads, int window) {
   // sequence, 8 key/value heads, 4096 tokens: 256 rows 24.6 us against 34.5 in tiles of 256, 384 rows about even;
   // 8 sequences: 64 rows 31.6 against 46.9, 128 rows 57.9 against 54.5
   p.prompt = rows > 64 && heads_all * ((rows + 15) / 16) > kCus;
-  p.tile_rows = p.prompt ? 256 : 16;
+  // 128 rows a workgroup where 256 leave CUs idle and the rows' own tokens are most of what they see, so that the last
+  // tiles take longest: one prompt of 32 over 8 heads, 512 tokens 21.4 us against 27.0 in tiles of 256, 1024 32.7 and
+  // 43.1, 2048 (two workgroups a CU) 67.8 and 75.5. Not for short prompts in two workgroups a CU (four of 512: 38.4
+  // and 29.7), nor on a long context, which is split evenly (512 tokens on 8192: 108 and 96).
+  const int64_t wide = heads_all * ((rows + 255) / 256);
+  const bool narrow = int64_t(b.max_pages) * c.page <= 2 * int64_t(b.max_q) && wide <= (b.max_q >= 1024 ? kCus : kCus / 2);
+  p.tile_rows = !p.prompt ? 16 : narrow ? 128 : 256;
   p.tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
   int64_t longest = int64_t(b.max_pages) * c.page;
   if (window > 0) longest = std::min<int64_t>(longest, int64_t(window) + b.max_q + 63);
   // The context is split while that leaves one workgroup a CU at most, and a split has enough tokens to pay for the
   // joining launch (single tokens, 32 over 8 heads: 1024 tokens 11.4 us in two of 512, 11.8 whole; 64 channels: 9.3
   // and 7.6). More workgroups than that are never split, not even where the last tiles of a prompt outlast the
-  // others: 2048 tokens, 32 over 8 heads, 256 workgroups of 1 to 32 chunks in parts of 17 took 87 us and 16 more to
-  // join, whole 77 (workgroups start in order, in rotation over the shader engines, so long and short ones in turn
-  // end up on the same CUs).
+  // others: 2048 tokens, 32 over 8 heads, 256 workgroups of 256 rows and 1 to 32 chunks, in parts of 17, took 87 us and
+  // 16 more to join, whole 77 (workgroups start in order, in rotation over the shader engines, so long and short ones
+  // in turn end up on the same CUs).
   const int64_t most = std::max<int64_t>(1, kCus / (heads_all * p.tiles)), least = p.prompt ? 512 : 65536 / c.head_dim;
   p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (longest + least - 1) / least)));
   if (window > 0) p.splits = std::min(p.splits, plan(c, b, heads, 0).splits);   // fits in the workspace of window 0
@@ -833,7 +881,8 @@ kq_status launch(const AttnArgs& a, bool prompt, hipStream_t st) {
   kq_status r;
   if (prompt) {
     LaunchTimer timer("cache_prompt_kernel", st);
-    hipLaunchKernelGGL((cache_prompt_kernel<BF16, D>), grid, dim3(512), 0, st, a);
+    if (a.tile_rows == 128) hipLaunchKernelGGL((cache_prompt_kernel<BF16, D, 128>), grid, dim3(512), 0, st, a);
+    else hipLaunchKernelGGL((cache_prompt_kernel<BF16, D, 256>), grid, dim3(512), 0, st, a);
     r = check_launch("cache_prompt_kernel");
   } else {
     LaunchTimer timer("cache_token_kernel", st);

@@ -446,6 +446,24 @@ def test_attention_prompts(dtype, heads, kvh, dim, page, lens, news):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("heads,kvh,dim,page,length,new,window", [
+    (16, 4, 128, 16, 300, 300, 0), (16, 4, 64, 64, 417, 289, 0), (8, 8, 128, 32, 700, 650, 90), (6, 6, 64, 16, 1100, 1100, 0),
+    (16, 4, 128, 128, 250, 270, 33),
+])
+def test_attention_prompt_tiles(dtype, wide, heads, kvh, dim, page, length, new, window):
+    """Few workgroups: in a table that holds little more than the prompt, rows in tiles of 128 with two waves for each 32;
+    in one that could hold a long context before it, tiles of 256, split. The last case has rows without a token."""
+    rng = np.random.default_rng(length)
+    table, pages = tables(rng, [length], page)
+    if wide:
+        table = np.concatenate((table, np.full((1, 4 * new // page + 1), -7, np.int32)), 1)
+    _, info = attention_case(new, dtype, heads, kvh, dim, page, [length], [new], window=window, table=table,
+                             cache=filled(rng, pages, page, kvh, dim))
+    assert info == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 65, 300, 2 ** 31 - 1])
 def test_attention_window(dtype, window):
     attention_case(window % 97, dtype, 8, 2, 128, 16, [1, 40, 333, 500], [1, 1, 3, 1], window=window)
