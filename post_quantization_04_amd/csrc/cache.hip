@@ -9,7 +9,7 @@
 // 16-byte store for each of its channels. Queries need no scale and go to workgroups of their
 // own, a wave for each token and group of heads.
 //
-// Three prompts of up to 8192 tokens, 32 over 8 heads, bf16 (554 MB): 172 us, 3.2 TB/s; all in
+// Three prompts of up to 8192 tokens, 32 over 8 heads, bf16 (519 MB): 172 us, 3.0 TB/s; all in
 // float32 it would be 157. Few tokens are latency: table entry, old scale, row, norm's sum, the
 // block's maximum and the code follow from one another (one token 3.9 us, 64 of them 12.1).
 //

@@ -168,9 +168,9 @@ __device__ __forceinline__ Range chunk_range(const AttnArgs& a, const Seq& s, in
 //
 // Bound by HBM where the context is long: 64 tokens over up to 8191, 32 heads each (2.6 GB of
 // codes), 467 us, 5.6 TB/s; one token over 131070, 64 over 8 heads (268 MB), 51 us, and 4 to join
-// its parts. Short ones are latency: 300 tokens, 8.0 us, of which an empty launch is about 2.
-// Eight waves a workgroup, not four: the join in LDS is cheaper than twice the parts to join
-// from memory, and two workgroups a CU keep 32 KB of loads in flight each.
+// its parts. Short ones are latency: 300 tokens, 8.0 us. Eight waves a workgroup, joined in LDS,
+// and one workgroup a CU leave half the parts to join from memory that four waves and two
+// workgroups do (131070 tokens 54.9 us and 61.5, 300 tokens 8.2 and 8.7).
 // ---------------------------------------------------------------------------
 template <bool BF16, int D>
 __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnArgs a) {
