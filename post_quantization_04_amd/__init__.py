@@ -465,7 +465,7 @@ class KVCache:
     v [pages, kv_heads, page / 16, head_dim, 16] (16 tokens of a channel side by side) with float32 scales
     k_scale, v_scale [pages, kv_heads]. Holds the tensors; the calls write into them."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "device", "kv_heads", "head_dim", "page", "struct", "ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "device", "gpu", "kv_heads", "head_dim", "page", "struct", "ref")
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
@@ -481,6 +481,7 @@ class KVCache:
               "KVCache: tensors must be contiguous and on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device, self.kv_heads, self.head_dim, self.page = k.device, heads, dim, page
+        self.gpu = k.device.index if k.device.type == "cuda" else None
         self.struct = CacheStruct(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), pages, page, heads, dim)
         self.ref = ctypes.byref(self.struct)
 
@@ -527,12 +528,14 @@ def _cache_tensor(name: str, t, heads: int, cache: KVCache, rows: Optional[int] 
     """(rows, row pitch) of a [rows, heads, head_dim] tensor of a cache call. Called for every tensor of calls that
     take microseconds: the message is put together only for a tensor that is refused."""
     shape = t.shape
-    if len(shape) == 3 and t.device == cache.device and (dtype is None or t.dtype == dtype):
+    if len(shape) == 3 and t.device == cache.device and (dtype is None or t.dtype is dtype):
         n, h, d = shape
-        s0, s1, s2 = t.stride()
-        if (d == cache.head_dim and (h == heads or heads == 0) and (rows is None or n == rows) and s2 == 1
-                and (s1 == d or h == 1 or n == 0)):
-            return n, (s0 if n > 1 else h * d)
+        if d == cache.head_dim and (h == heads or heads == 0) and (rows is None or n == rows):
+            if n <= 1 and t.is_contiguous():
+                return n, h * d
+            s0, s1, s2 = t.stride()
+            if s2 == 1 and (s1 == d or h == 1 or n == 0):
+                return n, (s0 if n > 1 else h * d)
     _need(len(shape) == 3 and shape[2] == cache.head_dim and (heads == 0 or shape[1] == heads)
           and (rows is None or shape[0] == rows), f"{name}: must be [rows, heads, head_dim]")
     _need(dtype is None or t.dtype == dtype, f"{name}: dtype differs")
@@ -562,18 +565,18 @@ def _cache_info(name: str, info, cache: KVCache):
 
 def _cache_call(name: str, fn, cache: KVCache, batch: CacheBatch, args, stream) -> None:
     """fn(cache, batch, *args, stream) on the cache's device, whichever device is current."""
-    torch, device = _torch, cache.device
-    if device.type != "cuda" or batch.device != device:
+    gpu, C = cache.gpu, _torch._C
+    if gpu is None or batch.device != cache.device:
         raise KQError(KQ_EINVAL, f"{name}: cache and batch must be on one GPU")
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)  # current_stream(device).cuda_stream without the object
+        raw = C._cuda_getCurrentRawStream(gpu)  # current_stream(device).cuda_stream without the object
     else:
-        _need(stream.device == device, f"{name}: the stream belongs to another device")
+        _need(stream.device == cache.device, f"{name}: the stream belongs to another device")
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if C._cuda_getDevice() == gpu:
         status = fn(cache.ref, batch.ref, *args, raw)
     else:
-        with torch.cuda.device(device):
+        with _torch.cuda.device(gpu):
             status = fn(cache.ref, batch.ref, *args, raw)
     if status != KQ_OK:
         _check(status, name)
