@@ -167,8 +167,8 @@ __device__ __forceinline__ Range chunk_range(const AttnArgs& a, const Seq& s, in
 // bytes a lane.
 //
 // Bound by HBM where the context is long: 64 tokens over up to 8191, 32 heads each (2.6 GB of
-// codes), 467 us, 5.6 TB/s; one token over 131070, 64 over 8 heads (268 MB), 51 us, and 4 to join
-// its parts. Short ones are latency: 300 tokens, 8.0 us. Eight waves a workgroup, joined in LDS,
+// codes), 461 us, 5.7 TB/s; one token over 131070, 64 over 8 heads (268 MB), 51 us, and 4 to join
+// its parts. Short ones are latency: 300 tokens, 7.9 us. Eight waves a workgroup, joined in LDS,
 // and one workgroup a CU leave half the parts to join from memory that four waves and two
 // workgroups do (131070 tokens 54.9 us and 61.5, 300 tokens 8.2 and 8.7).
 // ---------------------------------------------------------------------------
@@ -201,45 +201,6 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
   // every token of a chunk is seen by every row if it lies in (p_last - window, p_first]
   const int p_first = first + i_first, p_last = first + i_last;
 
-  // the row of q in float16 pieces, in the channel order of the key loads
-  half8 qh[2 * U], ql[BF16 ? 1 : 2 * U];
-  float down;
-  {
-    const int64_t at = (int64_t(s.row0) + i) * a.ldq + int64_t(hd) * D;
-    float x[2 * U][8];
-    float amax = 0.0f, odd = 0.0f;
-#pragma unroll
-    for (int t = 0; t < 2 * U; ++t) {
-      load8<BF16>(a.q, at + 64 * (t >> 1) + 16 * lk + 8 * (t & 1), x[t]);
-    }
-#pragma unroll
-    for (int t = 0; t < 2 * U; ++t)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        amax = fmaxf(amax, fabsf(x[t][j]));
-        odd = fmaf(x[t][j], 0.0f, odd);          // NaN once an entry is not finite
-      }
-    amax = odd == odd ? amax : INFINITY;
-    amax = fmaxf(amax, __shfl_xor(amax, 16));
-    amax = fmaxf(amax, __shfl_xor(amax, 32));
-    float up;
-    row_scale(amax, up, down);
-#pragma unroll
-    for (int t = 0; t < 2 * U; ++t)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float y = x[t][j] * up;
-        const _Float16 h = _Float16(y);
-        qh[t][j] = h;
-        if (!BF16) ql[t][j] = _Float16(y - float(h));
-      }
-  }
-  const float qf = a.scale_log2e * down;
-
-  floatx4 o[DT];
-#pragma unroll
-  for (int t = 0; t < DT; ++t) o[t] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-  float m = kNoToken, l = 0.0f;
   const int page = 1 << a.seq.page_log2, pmask = page - 1;
 
   // Codes are loaded into the registers of the chunk before as soon as its products have used them, their pages
@@ -272,7 +233,53 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
 #pragma unroll
     for (int t = 0; t < DT; ++t) vc[t] = *reinterpret_cast<const uint4*>(vp + 256 * t);
   };
-  bool known = true;                             // whether this lane's block is a page, for the chunk in registers
+  // The first chunk's table entries, the queries and the chunk's codes are under way before the queries are waited for.
+  // A wave without a chunk loads what the others do.
+  int c = rg.c0 + wave;
+  look(c);
+  // the row of q; its float16 pieces are in the channel order of the key loads
+  float qx[2 * U][8];
+  {
+    const int64_t at = (int64_t(s.row0) + i) * a.ldq + int64_t(hd) * D;
+#pragma unroll
+    for (int t = 0; t < 2 * U; ++t) load8<BF16>(a.q, at + 64 * (t >> 1) + 16 * lk + 8 * (t & 1), qx[t]);
+  }
+  load_keys();
+  load_values();
+  bool known = is_page(a.seq, idv);              // whether this lane's block is a page, for the chunk in registers
+  look(c + W);
+  half8 qh[2 * U], ql[BF16 ? 1 : 2 * U];
+  float down;
+  {
+    float amax = 0.0f, odd = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 2 * U; ++t)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        amax = fmaxf(amax, fabsf(qx[t][j]));
+        odd = fmaf(qx[t][j], 0.0f, odd);         // NaN once an entry is not finite
+      }
+    amax = odd == odd ? amax : INFINITY;
+    amax = fmaxf(amax, __shfl_xor(amax, 16));
+    amax = fmaxf(amax, __shfl_xor(amax, 32));
+    float up;
+    row_scale(amax, up, down);
+#pragma unroll
+    for (int t = 0; t < 2 * U; ++t)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float y = qx[t][j] * up;
+        const _Float16 h = _Float16(y);
+        qh[t][j] = h;
+        if (!BF16) ql[t][j] = _Float16(y - float(h));
+      }
+  }
+  const float qf = a.scale_log2e * down;
+
+  floatx4 o[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) o[t] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = kNoToken, l = 0.0f;
   // one chunk; every load is unconditional, so that the waits count those that are still out
   auto chunk = [&](int c, auto more) {
     floatx4 e[4];
@@ -354,13 +361,7 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void cache_token_kernel(AttnAr
       look(c + 2 * W);
     }
   };
-  int c = rg.c0 + wave;
   if (c < rg.c1) {
-    look(c);
-    load_keys();
-    load_values();
-    known = is_page(a.seq, idv);
-    look(c + W);
     for (; c + W < rg.c1; c += W) chunk(c, std::true_type{});
     chunk(c, std::false_type{});
   }
