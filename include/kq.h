@@ -580,7 +580,7 @@ kq_status kq_cache_read(const kq_cache* cache, const kq_cache_batch* batch, void
  *   out      device, same shape and type, row pitch ldo; must not overlap q
  *            (16-byte aligned, pitches multiples of 16 bytes)
  *   heads    a multiple of kv_heads
- *   scale    finite and > 0; window >= 0
+ *   scale    > 0, below 2e38; window >= 0
  *   info     as kq_cache_append (rows past max_q of a sequence are left as they were)
  *   ws       kq_cache_attention_workspace bytes; calls sharing it must not overlap.
  * Tokens of a bad page count as NaN, and so do scores (scale q . k) past

@@ -482,7 +482,8 @@ kq_status kq_cache_attention(const kq_cache* cache, const kq_cache_batch* batch,
   if ((st = cache_pointers(what, cache, batch)) != KQ_OK) return st;
   if (heads < 1 || heads > 65536 || heads % cache->kv_heads)
     return fail(KQ_EINVAL, "%s: heads %d is not a multiple of kv_heads %d", what, heads, cache->kv_heads);
-  if (!(scale > 0.0f && std::isfinite(scale))) return fail(KQ_EINVAL, "%s: scale must be finite and > 0", what);
+  if (!(scale > 0.0f && std::isfinite(scale * 1.5f)))  // 1.5 > log2 e, which the kernels multiply it by
+    return fail(KQ_EINVAL, "%s: scale must be finite (below 2e38) and > 0", what);
   if (window < 0) return fail(KQ_EINVAL, "%s: window %d < 0", what, window);
   if ((st = cache_tensor(what, "q", q, dtype, rows, heads, cache->head_dim, ldq)) != KQ_OK) return st;
   if ((st = cache_tensor(what, "out", out, dtype, rows, heads, cache->head_dim, ldo)) != KQ_OK) return st;

@@ -103,6 +103,11 @@ def test_attention_refusals(L, at, value):
     assert L.kq_cache_attention(ctypes.byref(_cache()), ctypes.byref(_batch()), *_with(ATTEND, at, value)) == kq.KQ_EINVAL
 
 
+def test_attention_scale_in_base_two_is_finite(L):
+    """Exponents are in base 2: a finite scale whose product with log2 e is not finite would make zero scores NaN."""
+    assert L.kq_cache_attention(ctypes.byref(_cache()), ctypes.byref(_batch()), *_with(ATTEND, 5, 3.0e38)) == kq.KQ_EINVAL
+
+
 def test_attention_small_workspace(L):
     cache, batch = _cache(), _batch(max_pages=2000)
     need = L.kq_cache_attention_workspace(ctypes.byref(cache), ctypes.byref(batch), kq.KQ_F32, 4, 32, 0)
